@@ -6,7 +6,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_b200.so")
-SOURCES = ["moe_api.cu", "route.cu", "combine.cu", "gemm_tc.cu"]
+SOURCES = ["moe_api.cu", "route.cu", "combine.cu", "gemm_tc.cu", "balance.cu",
+           "norm.cu", "w4.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

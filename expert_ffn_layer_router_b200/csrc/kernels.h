@@ -95,4 +95,42 @@ cudaError_t launch_router_gemm(const void* x, int T, int d, const float* Wr, con
 void launch_router_split(const float* Wr, int d, int E, void* split_buf, int32_t* zero,
                          int zero_n, cudaStream_t s, int* launches);
 
+// balance.cu
+// Router losses: losses [2], counts [E+1] (pairs per expert, then tokens), probs [E].  mask
+// (nullable): 0 leaves a token out.  part: balance_scratch_bytes(T, E) bytes.
+size_t balance_scratch_bytes(int T, int E);
+void launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, int T, int E,
+                    int k, float* part, float* losses, int32_t* counts, float* probs,
+                    DeviceStatus* st, cudaStream_t s, int* launches);
+// Gradient of the losses (grad_losses, nullable) and of the routing weights (grad_w, nullable)
+// with respect to the logits.
+void launch_route_backward(const float* logits, const int32_t* ids, const uint8_t* mask,
+                           const int32_t* counts, const float* grad_losses, const float* grad_w,
+                           int T, int E, int k, bool renorm, float* dlogits, DeviceStatus* st,
+                           cudaStream_t s, int* launches);
+
+// norm.cu
+void launch_layer_norm(int dtype, const void* x, const float* gamma, const float* beta, float eps,
+                       int rows, int d, void* y, float* mean, float* rstd, cudaStream_t s,
+                       int* launches);
+// part: layer_norm_scratch_bytes(rows, d) bytes; dres nullable (added to dx).
+size_t layer_norm_scratch_bytes(int rows, int d);
+void launch_layer_norm_backward(int dtype, const void* dy, const void* x, const float* gamma,
+                                const float* mean, const float* rstd, const void* dres, int rows,
+                                int d, void* dx, float* dgamma, float* dbeta, float* part,
+                                cudaStream_t s, int* launches);
+
+// w4.cu
+void launch_w4_quantize(int dtype, const void* W, int E, int N, int K, int G, uint32_t* q,
+                        uint16_t* scale, uint16_t* zero, cudaStream_t s, int* launches);
+void launch_w4_dequantize(const uint32_t* q, const uint16_t* scale, const uint16_t* zero, int E,
+                          int N, int K, int G, void* W, cudaStream_t s, int* launches);
+// Grouped products over 4-bit weights [E, N, K] for few rows per expert.  which = 0: D = SiLU(A
+// W^T + bias), 1: D = A W^T + bias, 2: gated (N = 2 F rows of W, F columns of D).
+cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int a_row_limit,
+                           const int32_t* offsets, int E, int K, int N, int max_rows,
+                           const uint32_t* q, const uint16_t* scale, const uint16_t* zero, int G,
+                           const float* bias, void* D, int ldd, DeviceStatus* st, cudaStream_t s,
+                           int* launches);
+
 }  // namespace moe

@@ -63,7 +63,7 @@ long long max_rows_of(const moe_problem* p, long long K) {
 
 struct Plan {
     size_t status, gcnt, logits, ids, w, slot, drop, counts, cand, bits, offsets, rowtok,
-        kept_tmp, H, Y, split, total;
+        kept_tmp, H, Y, split, part, total;
 };
 
 Plan make_plan(const moe_problem* p) {
@@ -93,6 +93,9 @@ Plan make_plan(const moe_problem* p) {
     q.H = take(R * p->d_ff * esize(p));
     q.Y = take(R * p->d_model * esize(p));
     q.split = take(p->dtype == MOE_BF16 ? moe::router_split_bytes(p->d_model, p->E) : 0);
+    // Partial sums of the router losses and of the layer norm's parameter gradients.
+    q.part = take(std::max(moe::balance_scratch_bytes(p->T, p->E),
+                           moe::layer_norm_scratch_bytes(p->T, p->d_model)));
     q.total = off;
     return q;
 }
@@ -188,6 +191,75 @@ moe_status ffn_steps(const moe_problem* p, const void* x, const int32_t* offsets
     return MOE_OK;
 }
 
+// ---- 4-bit weights ----
+bool bad_group(int32_t g) { return g != 32 && g != 64 && g != 128; }
+
+bool bad_w4(const moe_w4* w) {
+    return !w || !w->q || !w->scale || bad_group(w->group) || misaligned(w->q, 16) ||
+           misaligned(w->scale, 16) || misaligned(w->zero, 16);
+}
+
+int w4_rows1(const moe_problem* p) {          // rows of W1 per expert
+    return (p->flags & MOE_FLAG_GATED) ? 2 * p->d_ff : p->d_ff;
+}
+
+// Rows per expert (the batch's largest average) up to which the products read the 4-bit weights
+// directly; above it the weights are first read back to bfloat16 for the tensor-core GEMM.
+constexpr long long kW4DirectRows = 96;
+
+bool w4_direct(const moe_problem* p) {
+    return max_rows_of(p, capacity_of(p)) <= kW4DirectRows * p->E;
+}
+
+constexpr int32_t kW4MaxRows = 32 * 65535;    // row tiles of 32 on one grid axis
+
+// bfloat16 copy of one of the two weights (they are used one after the other).
+size_t w4_copy_bytes(const moe_problem* p) {
+    if (w4_direct(p)) return 0;
+    return align_up((size_t)p->E * std::max(w4_rows1(p), p->d_ff) * p->d_model * 2);
+}
+
+moe_status ffn_w4_steps(const moe_problem* p, const void* x, const int32_t* offsets,
+                        const int32_t* rowtok, const moe_w4* W1, const float* b1,
+                        const moe_w4* W2, const float* b2, void* Y, void* ws, const Plan& q,
+                        cudaStream_t s, int* launches) {
+    moe::DeviceStatus* st = at<moe::DeviceStatus>(ws, q.status);
+    const long long R = max_rows_of(p, capacity_of(p));
+    if (R == 0) return MOE_OK;
+    const int g1 = (p->flags & MOE_FLAG_GATED) ? 2 : 0, N1 = w4_rows1(p);
+    const int d = p->d_model, F = p->d_ff, E = p->E;
+    void* H = at<void>(ws, q.H);
+    cudaError_t e;
+    auto q1 = [](const moe_w4* w) { return (const uint32_t*)w->q; };
+    auto sc = [](const moe_w4* w) { return (const uint16_t*)w->scale; };
+    auto ze = [](const moe_w4* w) { return (const uint16_t*)w->zero; };
+    if (w4_direct(p)) {
+        e = moe::launch_w4_gemm(g1, x, rowtok, p->T, offsets, E, d, N1, (int)R, q1(W1), sc(W1),
+                                ze(W1), W1->group, b1, H, F, st, s, launches);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+        e = moe::launch_w4_gemm(1, H, nullptr, (int)R, offsets, E, F, d, (int)R, q1(W2), sc(W2),
+                                ze(W2), W2->group, b2, Y, d, st, s, launches);
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    void* W = at<void>(ws, q.total);
+    moe::launch_w4_dequantize(q1(W1), sc(W1), ze(W1), E, N1, d, W1->group, W, s, launches);
+    e = moe::launch_expert_gemm(g1, x, d, rowtok, p->T, offsets, E, d, F, W, b1, H, F, R, st, s,
+                                launches);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    moe::launch_w4_dequantize(q1(W2), sc(W2), ze(W2), E, d, F, W2->group, W, s, launches);
+    e = moe::launch_expert_gemm(1, H, F, nullptr, (int)R, offsets, E, F, d, W, b2, Y, d, R, st, s,
+                                launches);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// The experts' weights of a forward: bfloat16 / float32 (W1, W2) or 4-bit (Q1, Q2).
+struct ExpertWeights {
+    const void* W1;
+    const void* W2;
+    const moe_w4* Q1;
+    const moe_w4* Q2;
+};
+
 // ------------------------------------------------------------------------------------------------
 // moe_route_static: moe_route for callers that cannot allocate device memory.
 //
@@ -274,6 +346,105 @@ void* static_scratch_for_current_context(cudaError_t* err) {
         }
     }
     return ptr;
+}
+
+// Router, capacity, experts and combine: the layer reads x, the combine adds onto res.
+moe_status forward_steps(const moe_problem* p, const void* x, const void* res, const float* Wr,
+                         const float* br, const ExpertWeights& W, const float* b1,
+                         const float* b2, void* out, float* logits_out, int32_t* ids_out,
+                         float* w_out, int32_t* slot_out, uint8_t* drop_out, int32_t* counts_out,
+                         void* ws, const Plan& q, cudaStream_t s, int launches) {
+    moe_status r;
+    int32_t* counts = counts_out ? counts_out : at<int32_t>(ws, q.counts);
+    if (p->T == 0) {
+        moe::note_launch(cudaMemsetAsync(counts, 0, sizeof(int32_t) * 2 * p->E, s));
+        return finish(0);
+    }
+    moe::DeviceStatus* st = at<moe::DeviceStatus>(ws, q.status);
+    float* logits = logits_out ? logits_out : at<float>(ws, q.logits);
+    int32_t* ids = ids_out ? ids_out : at<int32_t>(ws, q.ids);
+    float* w = w_out ? w_out : at<float>(ws, q.w);
+    int32_t* slot = slot_out ? slot_out : at<int32_t>(ws, q.slot);
+    uint8_t* drop = drop_out ? drop_out : at<uint8_t>(ws, q.drop);
+    int32_t* offsets = at<int32_t>(ws, q.offsets);
+    int32_t* rowtok = at<int32_t>(ws, q.rowtok);
+    void* Y = at<void>(ws, q.Y);
+
+    stage_mark(0, s);
+    // Small bf16 batches: logits on CUDA cores and routing in one launch (a 128-row tensor-core
+    // tile would leave the GPU idle), then the single-block dispatch.  Larger batches: logits
+    // from the tensor cores (bf16) or CUDA cores (fp32), whose launch also clears the dispatch
+    // counters; then the router that places each pair in its expert's candidate list, and the
+    // per-expert capacity selection.
+    const bool small = p->dtype == MOE_BF16 && moe::router_small_fits(p->T, p->E, p->d_model);
+    const bool small_dispatch = moe::dispatch_small_fits(p->T, p->k);
+    int32_t* gcnt = small_dispatch ? nullptr : at<int32_t>(ws, q.gcnt);
+    const int zero_n = small_dispatch ? 0 : (int)moe::dispatch_counter_ints(p->E);
+    if (small) {
+        // The large dispatch re-reads the logits: keep them (in the workspace if not asked for).
+        moe::launch_router_small(x, Wr, br, p->T, p->d_model, p->E, p->k,
+                                 small_dispatch ? logits_out : logits, ids, w, p->flags, s,
+                                 &launches);
+        if (!small_dispatch) moe::note_launch(cudaMemsetAsync(gcnt, 0, sizeof(int32_t) * (size_t)zero_n, s));
+    } else if (p->dtype == MOE_BF16) {
+        if (moe::launch_router_gemm(x, p->T, p->d_model, Wr, br, p->E, at<void>(ws, q.split),
+                                    (p->flags & MOE_FLAG_ROUTER_PREPARED) != 0, logits, gcnt,
+                                    zero_n, st, s, &launches) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    } else {
+        moe::launch_logits_f32((const float*)x, Wr, br, p->T, p->d_model, p->E, logits, gcnt,
+                               zero_n, s, &launches);
+    }
+    stage_mark(1, s);
+    const long long K = capacity_of(p);
+    if (small_dispatch) {
+        if (!small) {
+            moe::launch_route_topk(logits, p->T, p->E, p->k, ids, w, s, p->flags);
+            launches += 1;
+        }
+        stage_mark(2, s);
+        moe::launch_dispatch_small(ids, w, p->T, p->E, p->k, K, p->flags, slot, drop, counts,
+                                   offsets, rowtok, st, s, &launches);
+    } else {
+        const RouteScratch rs = scratch_of(ws, q);
+        // (After the small router this routes the T <= 1024 tokens a second time, with the
+        // same arithmetic, to place the pairs.)
+        moe::launch_route_place(logits, p->T, p->E, p->k, p->flags, ids, w, gcnt, rs.cand, st,
+                                s, &launches);
+        stage_mark(2, s);
+        moe::launch_select(rs.cand, gcnt, w, p->T, p->E, p->k, K, p->flags, rs.bits, slot, drop,
+                           counts, offsets, rowtok, st, s, &launches);
+    }
+    stage_mark(3, s);
+    const long long R = max_rows_of(p, K);
+    if (W.Q1) {
+        r = ffn_w4_steps(p, x, offsets, rowtok, W.Q1, b1, W.Q2, b2, Y, ws, q, s, &launches);
+        if (r != MOE_OK) return r;
+        stage_mark(4, s);
+        stage_mark(5, s);
+    } else if (R > 0 && p->dtype == MOE_BF16) {
+        void* H = at<void>(ws, q.H);
+        const int g1 = (p->flags & MOE_FLAG_GATED) ? 2 : 0;
+        if (moe::launch_expert_gemm(g1, x, p->d_model, rowtok, p->T, offsets, p->E, p->d_model,
+                                    p->d_ff, W.W1, b1, H, p->d_ff, R, st, s, &launches) !=
+            cudaSuccess)
+            return MOE_ERR_CUDA;
+        stage_mark(4, s);
+        if (moe::launch_expert_gemm(1, H, p->d_ff, nullptr, (int)R, offsets, p->E, p->d_ff,
+                                    p->d_model, W.W2, b2, Y, p->d_model, R, st, s, &launches) !=
+            cudaSuccess)
+            return MOE_ERR_CUDA;
+        stage_mark(5, s);
+    } else {
+        r = ffn_steps(p, x, offsets, rowtok, W.W1, b1, W.W2, b2, Y, ws, q, s, &launches);
+        if (r != MOE_OK) return r;
+        stage_mark(4, s);
+        stage_mark(5, s);
+    }
+    moe::launch_combine(p->dtype, res, Y, w, ids, slot, offsets, p->T, p->d_model, p->E, p->k, R,
+                        out, st, s, &launches);
+    stage_mark(6, s);
+    return finish(launches);
 }
 
 }  // namespace
@@ -466,93 +637,187 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
         return MOE_ERR_INVALID_ARG;
     Plan q;
     if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
+    return forward_steps(p, x, x, Wr, br, ExpertWeights{W1, W2, nullptr, nullptr}, b1, b2, out,
+                         logits_out, ids_out, w_out, slot_out, drop_out, counts_out, ws, q,
+                         (cudaStream_t)stream, 0);
+}
+
+moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes) {
+    if (bad_problem(p) || !bytes) return MOE_ERR_INVALID_ARG;
+    if (p->dtype != MOE_BF16 || unsupported(p)) return MOE_ERR_UNSUPPORTED;
+    *bytes = make_plan(p).total + w4_copy_bytes(p);
+    return MOE_OK;
+}
+
+moe_status moe_quantize_packed(const void* W, int32_t dtype, int32_t E, int32_t N, int32_t K,
+                           int32_t group, void* q, void* scale, void* zero, void* stream) {
+    if ((dtype != MOE_F32 && dtype != MOE_BF16) || E < 1 || N < 1 || K < 1 || bad_group(group))
+        return MOE_ERR_INVALID_ARG;
+    if (K % 64 != 0 || N > kW4MaxRows || E > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!W || !q || !scale || misaligned(W, 16) || misaligned(q, 16) || misaligned(scale, 16) ||
+        misaligned(zero, 16))
+        return MOE_ERR_INVALID_ARG;
+    cudaGetLastError();
+    moe::g_launch_error = cudaSuccess;
+    int launches = 0;
+    moe::launch_w4_quantize(dtype, W, E, N, K, group, (uint32_t*)q, (uint16_t*)scale,
+                            (uint16_t*)zero, (cudaStream_t)stream, &launches);
+    return finish(launches);
+}
+
+moe_status moe_dequantize_packed(const moe_w4* w, int32_t E, int32_t N, int32_t K, void* W,
+                             void* stream) {
+    if (bad_w4(w) || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+    if (K % 64 != 0 || N > kW4MaxRows || E > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!W || misaligned(W, 16)) return MOE_ERR_INVALID_ARG;
+    cudaGetLastError();
+    moe::g_launch_error = cudaSuccess;
+    int launches = 0;
+    moe::launch_w4_dequantize((const uint32_t*)w->q, (const uint16_t*)w->scale,
+                              (const uint16_t*)w->zero, E, N, K, w->group, W,
+                              (cudaStream_t)stream, &launches);
+    return finish(launches);
+}
+
+moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int32_t* offsets,
+                             const int32_t* rowtok, const moe_w4* W1, const float* b1,
+                             const moe_w4* W2, const float* b2, void* Y, void* ws,
+                             size_t ws_bytes, void* stream) {
+    moe_status r = pre(p, true);
+    if (r != MOE_OK) return r;
+    if (p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (!offsets || bad_w4(W1) || bad_w4(W2) || (p->T > 0 && (!x || !rowtok || !Y)))
+        return MOE_ERR_INVALID_ARG;
+    if (misaligned(x, 16) || misaligned(Y, 16) || misaligned(b1, 16) || misaligned(b2, 16))
+        return MOE_ERR_INVALID_ARG;
+    Plan q;
+    if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
+    if (ws_bytes < q.total + w4_copy_bytes(p)) return MOE_ERR_WORKSPACE;
+    int launches = 0;
+    if (p->T == 0) return finish(0);
+    r = ffn_w4_steps(p, x, offsets, rowtok, W1, b1, W2, b2, Y, ws, q, (cudaStream_t)stream,
+                     &launches);
+    return r != MOE_OK ? r : finish(launches);
+}
+
+moe_status moe_layer_norm(const moe_problem* p, const void* x, const float* gamma,
+                          const float* beta, float eps, void* y, float* mean, float* rstd,
+                          void* stream) {
+    moe_status r = pre(p, false);
+    if (r != MOE_OK) return r;
+    if (!gamma || !beta || !(eps >= 0.0f) || std::isinf(eps) ||
+        (p->T > 0 && (!x || !y || !mean || !rstd)))
+        return MOE_ERR_INVALID_ARG;
+    if (y && y == x) return MOE_ERR_INVALID_ARG;
+    int launches = 0;
+    if (p->T > 0)
+        moe::launch_layer_norm(p->dtype, x, gamma, beta, eps, p->T, p->d_model, y, mean, rstd,
+                               (cudaStream_t)stream, &launches);
+    return finish(launches);
+}
+
+moe_status moe_layer_norm_backward(const moe_problem* p, const void* dy, const void* x,
+                                   const float* gamma, const float* mean, const float* rstd,
+                                   const void* dres, void* dx, float* dgamma, float* dbeta,
+                                   void* ws, size_t ws_bytes, void* stream) {
+    moe_status r = pre(p, false);
+    if (r != MOE_OK) return r;
+    if (!gamma || !dgamma || !dbeta || (p->T > 0 && (!dy || !x || !mean || !rstd || !dx)))
+        return MOE_ERR_INVALID_ARG;
+    if (dx && (dx == x || dx == dy || dx == dres)) return MOE_ERR_INVALID_ARG;
+    Plan q;
+    if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
     cudaStream_t s = (cudaStream_t)stream;
     int launches = 0;
-    int32_t* counts = counts_out ? counts_out : at<int32_t>(ws, q.counts);
     if (p->T == 0) {
-        moe::note_launch(cudaMemsetAsync(counts, 0, sizeof(int32_t) * 2 * p->E, s));
+        moe::note_launch(cudaMemsetAsync(dgamma, 0, sizeof(float) * p->d_model, s));
+        moe::note_launch(cudaMemsetAsync(dbeta, 0, sizeof(float) * p->d_model, s));
         return finish(0);
     }
-    moe::DeviceStatus* st = at<moe::DeviceStatus>(ws, q.status);
-    float* logits = logits_out ? logits_out : at<float>(ws, q.logits);
-    int32_t* ids = ids_out ? ids_out : at<int32_t>(ws, q.ids);
-    float* w = w_out ? w_out : at<float>(ws, q.w);
-    int32_t* slot = slot_out ? slot_out : at<int32_t>(ws, q.slot);
-    uint8_t* drop = drop_out ? drop_out : at<uint8_t>(ws, q.drop);
-    int32_t* offsets = at<int32_t>(ws, q.offsets);
-    int32_t* rowtok = at<int32_t>(ws, q.rowtok);
-    void* Y = at<void>(ws, q.Y);
-
-    stage_mark(0, s);
-    // Small bf16 batches: logits on CUDA cores and routing in one launch (a 128-row tensor-core
-    // tile would leave the GPU idle), then the single-block dispatch.  Larger batches: logits
-    // from the tensor cores (bf16) or CUDA cores (fp32), whose launch also clears the dispatch
-    // counters; then the router that places each pair in its expert's candidate list, and the
-    // per-expert capacity selection.
-    const bool small = p->dtype == MOE_BF16 && moe::router_small_fits(p->T, p->E, p->d_model);
-    const bool small_dispatch = moe::dispatch_small_fits(p->T, p->k);
-    int32_t* gcnt = small_dispatch ? nullptr : at<int32_t>(ws, q.gcnt);
-    const int zero_n = small_dispatch ? 0 : (int)moe::dispatch_counter_ints(p->E);
-    if (small) {
-        // The large dispatch re-reads the logits: keep them (in the workspace if not asked for).
-        moe::launch_router_small(x, Wr, br, p->T, p->d_model, p->E, p->k,
-                                 small_dispatch ? logits_out : logits, ids, w, p->flags, s,
-                                 &launches);
-        if (!small_dispatch) moe::note_launch(cudaMemsetAsync(gcnt, 0, sizeof(int32_t) * (size_t)zero_n, s));
-    } else if (p->dtype == MOE_BF16) {
-        if (moe::launch_router_gemm(x, p->T, p->d_model, Wr, br, p->E, at<void>(ws, q.split),
-                                    (p->flags & MOE_FLAG_ROUTER_PREPARED) != 0, logits, gcnt,
-                                    zero_n, st, s, &launches) != cudaSuccess)
-            return MOE_ERR_CUDA;
-    } else {
-        moe::launch_logits_f32((const float*)x, Wr, br, p->T, p->d_model, p->E, logits, gcnt,
-                               zero_n, s, &launches);
-    }
-    stage_mark(1, s);
-    const long long K = capacity_of(p);
-    if (small_dispatch) {
-        if (!small) {
-            moe::launch_route_topk(logits, p->T, p->E, p->k, ids, w, s, p->flags);
-            launches += 1;
-        }
-        stage_mark(2, s);
-        moe::launch_dispatch_small(ids, w, p->T, p->E, p->k, K, p->flags, slot, drop, counts,
-                                   offsets, rowtok, st, s, &launches);
-    } else {
-        const RouteScratch rs = scratch_of(ws, q);
-        // (After the small router this routes the T <= 1024 tokens a second time, with the
-        // same arithmetic, to place the pairs.)
-        moe::launch_route_place(logits, p->T, p->E, p->k, p->flags, ids, w, gcnt, rs.cand, st,
-                                s, &launches);
-        stage_mark(2, s);
-        moe::launch_select(rs.cand, gcnt, w, p->T, p->E, p->k, K, p->flags, rs.bits, slot, drop,
-                           counts, offsets, rowtok, st, s, &launches);
-    }
-    stage_mark(3, s);
-    const long long R = max_rows_of(p, K);
-    if (R > 0 && p->dtype == MOE_BF16) {
-        void* H = at<void>(ws, q.H);
-        const int g1 = (p->flags & MOE_FLAG_GATED) ? 2 : 0;
-        if (moe::launch_expert_gemm(g1, x, p->d_model, rowtok, p->T, offsets, p->E, p->d_model,
-                                    p->d_ff, W1, b1, H, p->d_ff, R, st, s, &launches) !=
-            cudaSuccess)
-            return MOE_ERR_CUDA;
-        stage_mark(4, s);
-        if (moe::launch_expert_gemm(1, H, p->d_ff, nullptr, (int)R, offsets, p->E, p->d_ff,
-                                    p->d_model, W2, b2, Y, p->d_model, R, st, s, &launches) !=
-            cudaSuccess)
-            return MOE_ERR_CUDA;
-        stage_mark(5, s);
-    } else {
-        r = ffn_steps(p, x, offsets, rowtok, W1, b1, W2, b2, Y, ws, q, s, &launches);
-        if (r != MOE_OK) return r;
-        stage_mark(4, s);
-        stage_mark(5, s);
-    }
-    moe::launch_combine(p->dtype, x, Y, w, ids, slot, offsets, p->T, p->d_model, p->E, p->k, R,
-                        out, st, s, &launches);
-    stage_mark(6, s);
+    moe::launch_layer_norm_backward(p->dtype, dy, x, gamma, mean, rstd, dres, p->T, p->d_model,
+                                    dx, dgamma, dbeta, at<float>(ws, q.part), s, &launches);
     return finish(launches);
+}
+
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* ids,
+                            const uint8_t* mask, float* losses, int32_t* counts, float* probs,
+                            void* ws, size_t ws_bytes, void* stream) {
+    moe_status r = pre(p, false);
+    if (r != MOE_OK) return r;
+    if (!losses || !counts || !probs || (p->T > 0 && (!logits || !ids)))
+        return MOE_ERR_INVALID_ARG;
+    Plan q;
+    if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
+    cudaStream_t s = (cudaStream_t)stream;
+    int launches = 0;
+    if (p->T == 0) {
+        moe::note_launch(cudaMemsetAsync(losses, 0, sizeof(float) * 2, s));
+        moe::note_launch(cudaMemsetAsync(counts, 0, sizeof(int32_t) * (p->E + 1), s));
+        moe::note_launch(cudaMemsetAsync(probs, 0, sizeof(float) * p->E, s));
+        return finish(0);
+    }
+    moe::launch_balance(logits, ids, mask, p->T, p->E, p->k, at<float>(ws, q.part), losses,
+                        counts, probs, at<moe::DeviceStatus>(ws, q.status), s, &launches);
+    return finish(launches);
+}
+
+moe_status moe_route_backward(const moe_problem* p, const float* logits, const int32_t* ids,
+                              const uint8_t* mask, const int32_t* counts,
+                              const float* grad_losses, const float* grad_w, float* dlogits,
+                              void* ws, size_t ws_bytes, void* stream) {
+    moe_status r = pre(p, false);
+    if (r != MOE_OK) return r;
+    if ((!grad_losses && !grad_w) || (grad_losses && !counts) || (grad_w && p->T > 0 && !ids) ||
+        (p->T > 0 && (!logits || !dlogits)) || (dlogits && dlogits == logits))
+        return MOE_ERR_INVALID_ARG;
+    Plan q;
+    if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
+    int launches = 0;
+    if (p->T > 0)
+        moe::launch_route_backward(logits, ids, mask, counts, grad_losses, grad_w, p->T, p->E,
+                                   p->k, (p->flags & MOE_FLAG_RENORMALIZE) != 0, dlogits,
+                                   at<moe::DeviceStatus>(ws, q.status), (cudaStream_t)stream,
+                                   &launches);
+    return finish(launches);
+}
+
+moe_status moe_forward_block(const moe_problem* p, const void* x, const moe_norm* norm,
+                             const float* Wr, const float* br, const void* W1, const void* W2,
+                             const moe_w4* Q1, const moe_w4* Q2, const float* b1,
+                             const float* b2, void* out, float* logits_out, int32_t* ids_out,
+                             float* w_out, int32_t* slot_out, uint8_t* drop_out,
+                             int32_t* counts_out, void* ws, size_t ws_bytes, void* stream) {
+    moe_status r = pre(p, true);
+    if (r != MOE_OK) return r;
+    const bool w4 = Q1 || Q2;
+    if (w4 && p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (!Wr || (p->T > 0 && (!x || !out)) || (out && out == x)) return MOE_ERR_INVALID_ARG;
+    if (w4 ? (W1 || W2 || bad_w4(Q1) || bad_w4(Q2)) : (!W1 || !W2)) return MOE_ERR_INVALID_ARG;
+    if (norm) {
+        if (!norm->gamma || !norm->beta || !(norm->eps >= 0.0f) || std::isinf(norm->eps) ||
+            (p->T > 0 && (!norm->y || !norm->mean || !norm->rstd)))
+            return MOE_ERR_INVALID_ARG;
+        if (norm->y && (norm->y == x || norm->y == out)) return MOE_ERR_INVALID_ARG;
+        if (p->dtype == MOE_BF16 && misaligned(norm->y, 16)) return MOE_ERR_INVALID_ARG;
+    }
+    if (p->dtype == MOE_BF16 &&
+        (misaligned(x, 16) || misaligned(W1, 16) || misaligned(W2, 16) || misaligned(out, 16) ||
+         misaligned(b1, 16) || misaligned(b2, 16)))
+        return MOE_ERR_INVALID_ARG;
+    Plan q;
+    if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
+    if (w4 && ws_bytes < q.total + w4_copy_bytes(p)) return MOE_ERR_WORKSPACE;
+    cudaStream_t s = (cudaStream_t)stream;
+    int launches = 0;
+    const void* xn = x;
+    if (norm && p->T > 0) {
+        moe::launch_layer_norm(p->dtype, x, norm->gamma, norm->beta, norm->eps, p->T, p->d_model,
+                               norm->y, norm->mean, norm->rstd, s, &launches);
+        xn = norm->y;
+    }
+    return forward_steps(p, xn, x, Wr, br, ExpertWeights{W1, W2, Q1, Q2}, b1, b2, out,
+                         logits_out, ids_out, w_out, slot_out, drop_out, counts_out, ws, q, s,
+                         launches);
 }
 
 moe_status moe_get_device_status(const void* ws, size_t ws_bytes, void* stream, int32_t* code) {

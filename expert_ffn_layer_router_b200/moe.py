@@ -7,6 +7,7 @@ There is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -19,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_b200.so")
 MOE_F32, MOE_BF16 = 0, 1
 FLAG_RENORMALIZE, FLAG_ARRIVAL_ORDER, FLAG_GATED, FLAG_ROUTER_PREPARED = 1, 2, 4, 8
 MOE_OK = 0
+MOE_ERR_INVALID_ARG = 1
 MOE_ERR_DEVICE = 5       # the status word holds an error (moe_get_device_status)
 DEV_OK, DEV_TIMEOUT, DEV_BAD_INDEX = 0, 1, 2
 
@@ -36,13 +38,25 @@ class Problem(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class W4(ctypes.Structure):
+    """moe_w4: device pointers of 4-bit weights and their group size."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("group", ctypes.c_int32)]
+
+
+class Norm(ctypes.Structure):
+    """moe_norm: parameters of the layer norm in front of a block, and where its results go."""
+    _fields_ = [("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("y", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError("libmoe_b200.so is not built (run __graft_entry__.build() or "
                           "python expert_ffn_layer_router_b200/build.py); there is no fallback")
     L = ctypes.CDLL(LIB_PATH)
-    P = ctypes.POINTER(Problem)
-    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    P, PW, PN = ctypes.POINTER(Problem), ctypes.POINTER(W4), ctypes.POINTER(Norm)
+    vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
     sig = {
         "moe_capacity": [P, ctypes.POINTER(ctypes.c_int64)],
         "moe_workspace_size": [P, ctypes.POINTER(ctypes.c_size_t)],
@@ -59,6 +73,15 @@ def _load():
         "moe_set_stage_events": [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32],
         "moe_route_static": [P, vp, vp, vp, vp, vp, vp, vp],
         "moe_selftest_wait_timeout": [vp, sz, ctypes.c_int32, vp],
+        "moe_quantize_packed": [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp],
+        "moe_dequantize_packed": [PW, i32, i32, i32, vp, vp],
+        "moe_workspace_size_packed": [P, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_expert_ffn_packed": [P, vp, vp, vp, PW, vp, PW, vp, vp, vp, sz, vp],
+        "moe_layer_norm": [P, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp],
+        "moe_layer_norm_backward": [P] + [vp] * 10 + [sz, vp],
+        "moe_balance_loss": [P] + [vp] * 7 + [sz, vp],
+        "moe_route_backward": [P] + [vp] * 8 + [sz, vp],
+        "moe_forward_block": [P, vp, PN, vp, vp, vp, vp, PW, PW] + [vp] * 10 + [sz, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -77,7 +100,10 @@ EXPORTS = ("moe_capacity", "moe_workspace_size", "moe_route", "moe_dispatch", "m
            "moe_combine", "moe_forward", "moe_get_device_status", "moe_reset_device_status",
            "moe_last_launch_count", "moe_status_string", "moe_set_stage_events",
            "moe_route_static", "moe_selftest_wait_timeout", "moe_capacity_dispatch",
-           "moe_router_logits", "moe_prepare_router")
+           "moe_router_logits", "moe_prepare_router", "moe_quantize_packed", "moe_dequantize_packed",
+           "moe_workspace_size_packed", "moe_expert_ffn_packed", "moe_layer_norm",
+           "moe_layer_norm_backward", "moe_balance_loss", "moe_route_backward",
+           "moe_forward_block")
 
 STAGE_EVENTS = 7
 STAGE_NAMES = ("router_logits", "route_topk", "capacity_dispatch", "expert_gemm1",
@@ -187,6 +213,75 @@ def moe_forward(p, x, Wr, br, W1, b1, W2, b2, out, ws, logits_out=None, ids_out=
            "moe_forward")
 
 
+def moe_workspace_size_packed(p: Problem) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.moe_workspace_size_packed(ctypes.byref(p), ctypes.byref(n)), "moe_workspace_size_packed")
+    return n.value
+
+
+def moe_quantize_packed(W, E, N, K, group, q, scale, zero=None, stream=None):
+    dtype = MOE_BF16 if W.dtype == torch.bfloat16 else MOE_F32
+    _check(_lib.moe_quantize_packed(_ptr(W), dtype, int(E), int(N), int(K), int(group), _ptr(q),
+                                _ptr(scale), _ptr(zero), _stream(stream)), "moe_quantize_packed")
+
+
+def moe_dequantize_packed(w: W4, E, N, K, W, stream=None):
+    _check(_lib.moe_dequantize_packed(ctypes.byref(w), int(E), int(N), int(K), _ptr(W),
+                                  _stream(stream)), "moe_dequantize_packed")
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def moe_expert_ffn_packed(p, x, offsets, rowtok, W1: W4, b1, W2: W4, b2, Y, ws, stream=None):
+    _check(_lib.moe_expert_ffn_packed(ctypes.byref(p), _ptr(x), _ptr(offsets), _ptr(rowtok),
+                                  _ref(W1), _ptr(b1), _ref(W2), _ptr(b2), _ptr(Y), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_expert_ffn_packed")
+
+
+def moe_layer_norm(p, x, gamma, beta, eps, y, mean, rstd, stream=None):
+    _check(_lib.moe_layer_norm(ctypes.byref(p), _ptr(x), _ptr(gamma), _ptr(beta), float(eps),
+                               _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream)),
+           "moe_layer_norm")
+
+
+def moe_layer_norm_backward(p, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, dres=None,
+                            stream=None):
+    _check(_lib.moe_layer_norm_backward(ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(gamma),
+                                        _ptr(mean), _ptr(rstd), _ptr(dres), _ptr(dx),
+                                        _ptr(dgamma), _ptr(dbeta), _ptr(ws),
+                                        ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_layer_norm_backward")
+
+
+def moe_balance_loss(p, logits, ids, losses, counts, probs, ws, mask=None, stream=None):
+    _check(_lib.moe_balance_loss(ctypes.byref(p), _ptr(logits), _ptr(ids), _ptr(mask),
+                                 _ptr(losses), _ptr(counts), _ptr(probs), _ptr(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_balance_loss")
+
+
+def moe_route_backward(p, logits, ids, counts, dlogits, ws, grad_losses=None, grad_w=None,
+                       mask=None, stream=None):
+    _check(_lib.moe_route_backward(ctypes.byref(p), _ptr(logits), _ptr(ids), _ptr(mask),
+                                   _ptr(counts), _ptr(grad_losses), _ptr(grad_w), _ptr(dlogits),
+                                   _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_route_backward")
+
+
+def moe_forward_block(p, x, norm, Wr, br, W1, W2, Q1, Q2, b1, b2, out, ws, logits_out=None,
+                      ids_out=None, w_out=None, slot_out=None, drop_out=None, counts_out=None,
+                      stream=None):
+    _check(_lib.moe_forward_block(ctypes.byref(p), _ptr(x), _ref(norm), _ptr(Wr), _ptr(br),
+                                  _ptr(W1), _ptr(W2), _ref(Q1), _ref(Q2), _ptr(b1), _ptr(b2),
+                                  _ptr(out), _ptr(logits_out), _ptr(ids_out), _ptr(w_out),
+                                  _ptr(slot_out), _ptr(drop_out), _ptr(counts_out), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_forward_block")
+
+
 def moe_get_device_status(ws, stream=None) -> int:
     """Status word of ``ws``; ``ws=None``: that of moe_route_static on the current device."""
     code = ctypes.c_int32()
@@ -222,17 +317,97 @@ def moe_set_stage_events(events):
 
 
 # ----------------------------------------------------------------------------------------------
+# Argument checks and streams of the tensor-level calls below
+# ----------------------------------------------------------------------------------------------
+def _need(what, name, t, dtype, shape, device):
+    """``t`` must be a dense tensor of this type and shape on ``device``."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or
+            t.device != device or not t.is_contiguous()):
+        raise MoeError(MOE_ERR_INVALID_ARG, "%s: %s must be a contiguous %s tensor of shape %s on %s"
+                       % (what, name, dtype, tuple(shape), device))
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Makes ``device`` and ``stream`` (None: the device's current stream) current, so results
+    allocated inside belong to the stream that writes them; yields the stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device)
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+class W4Weights:
+    """4-bit weights [E, N, K] with group scales: ``q`` [E, N, 16 ceil(K/128)] int32 words,
+    ``scale`` and the optional offsets ``zero`` [E, ceil(K/group), N] bfloat16 (the layout of
+    moe_w4).  :func:`quantize_w4` makes them."""
+
+    def __init__(self, q, scale, zero=None, *, K, group):
+        self.q, self.scale, self.zero = q, scale, zero
+        self.E, self.N, self.K, self.group = q.shape[0], q.shape[1], int(K), int(group)
+        if self.group not in (32, 64, 128):
+            raise MoeError(MOE_ERR_INVALID_ARG, "W4Weights: group must be 32, 64 or 128")
+        dev = q.device
+        _need("W4Weights", "q", q, torch.int32, (self.E, self.N, 16 * (-(-self.K // 128))), dev)
+        side = (self.E, -(-self.K // self.group), self.N)
+        _need("W4Weights", "scale", scale, torch.bfloat16, side, dev)
+        if zero is not None:
+            _need("W4Weights", "zero", zero, torch.bfloat16, side, dev)
+        self.c = W4(q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
+                    self.group)
+
+    def _need(self, what, name, shape, device):
+        if (self.E, self.N, self.K) != tuple(shape) or self.q.device != device:
+            raise MoeError(MOE_ERR_INVALID_ARG, "%s: %s must be 4-bit weights of shape %s on %s"
+                           % (what, name, tuple(shape), device))
+
+
+def quantize_w4(W, group, zeros=False, stream=None) -> W4Weights:
+    """Quantises ``W`` [E, N, K] (bfloat16 or float32, finite) to 4 bits with a scale, and with
+    ``zeros`` an offset, per ``group`` columns."""
+    if not isinstance(W, torch.Tensor) or W.dim() != 3 or W.dtype not in (torch.bfloat16,
+                                                                         torch.float32):
+        raise MoeError(MOE_ERR_INVALID_ARG, "quantize_w4: W must be bfloat16 or float32 [E, N, K]")
+    if group not in (32, 64, 128):
+        raise MoeError(MOE_ERR_INVALID_ARG, "quantize_w4: group must be 32, 64 or 128")
+    E, N, K = W.shape
+    _need("quantize_w4", "W", W, W.dtype, (E, N, K), W.device)
+    with _on(W.device, stream) as st:
+        q = torch.empty((E, N, 16 * (-(-K // 128))), dtype=torch.int32, device=W.device)
+        side = (E, -(-K // group), N)
+        scale = torch.empty(side, dtype=torch.bfloat16, device=W.device)
+        zero = torch.empty(side, dtype=torch.bfloat16, device=W.device) if zeros else None
+        moe_quantize_packed(W, E, N, K, group, q, scale, zero, st)
+    return W4Weights(q, scale, zero, K=K, group=group)
+
+
+def dequantize_w4(w: W4Weights, stream=None):
+    """The values of 4-bit weights, bfloat16 [E, N, K]."""
+    with _on(w.q.device, stream) as st:
+        W = torch.empty((w.E, w.N, w.K), dtype=torch.bfloat16, device=w.q.device)
+        moe_dequantize_packed(w.c, w.E, w.N, w.K, W, st)
+    return W
+
+
+# ----------------------------------------------------------------------------------------------
 # Convenience: a layer that owns its workspace (allocated once through torch).
 # ----------------------------------------------------------------------------------------------
 class MoELayer:
-    """Holds a problem description and a workspace; calls the C ABI on torch tensors."""
+    """Holds a problem description and a workspace; calls the C ABI on torch tensors.
+
+    ``w4``: size the workspace for 4-bit expert weights too (``expert_ffn_w4``,
+    ``forward_block`` with :class:`W4Weights`)."""
 
     def __init__(self, T, d_model, d_ff, E, k, capacity_factor=math.inf, dtype="bf16",
-                 device="cuda", flags=0):
+                 device="cuda", flags=0, w4=False):
         self.p = problem(T, d_model, d_ff, E, k, capacity_factor, dtype, flags)
         self.K = moe_capacity(self.p)
         self.device = torch.device(device)
-        nbytes = moe_workspace_size(self.p)
+        nbytes = moe_workspace_size_packed(self.p) if w4 else moe_workspace_size(self.p)
         # int64 elements keep the base 256-byte aligned through the caching allocator.
         self.ws = torch.zeros((nbytes + 7) // 8, dtype=torch.int64, device=self.device)
         self.max_rows = min(T * k, E * self.K)
@@ -313,3 +488,146 @@ class MoELayer:
         out = torch.empty_like(x)
         moe_combine(self.p, x, Y, w, ids, slot, offsets, out, self.ws, stream)
         return out
+
+    # -- router training ------------------------------------------------------------------------
+    def balance_loss(self, logits, ids, mask=None, stream=None):
+        """Router losses of a routing: ``losses`` [2] (load balance, z-loss), ``counts`` [E+1]
+        int32 (pairs per expert, then tokens), ``probs`` [E] (mean router probability).
+        ``mask`` [T] uint8 or bool: 0 leaves a token out."""
+        p, dev, what = self.p, self.ws.device, "balance_loss"
+        _need(what, "logits", logits, torch.float32, (p.T, p.E), dev)
+        _need(what, "ids", ids, torch.int32, (p.T, p.k), dev)
+        mask = self._mask(what, mask)
+        with _on(dev, stream) as st:
+            losses = torch.empty(2, dtype=torch.float32, device=dev)
+            counts = torch.empty(p.E + 1, dtype=torch.int32, device=dev)
+            probs = torch.empty(p.E, dtype=torch.float32, device=dev)
+            moe_balance_loss(p, logits, ids, losses, counts, probs, self.ws, mask, st)
+        return losses, counts, probs
+
+    def route_backward(self, logits, ids, counts=None, grad_losses=None, grad_w=None, mask=None,
+                       stream=None):
+        """dlogits [T, E] from the gradient of the losses (``grad_losses`` [2] on the device, with
+        ``counts`` from :meth:`balance_loss`) and of the routing weights (``grad_w`` [T, k])."""
+        p, dev, what = self.p, self.ws.device, "route_backward"
+        _need(what, "logits", logits, torch.float32, (p.T, p.E), dev)
+        _need(what, "ids", ids, torch.int32, (p.T, p.k), dev)
+        if grad_losses is not None:
+            _need(what, "grad_losses", grad_losses, torch.float32, (2,), dev)
+            _need(what, "counts", counts, torch.int32, (p.E + 1,), dev)
+        if grad_w is not None:
+            _need(what, "grad_w", grad_w, torch.float32, (p.T, p.k), dev)
+        mask = self._mask(what, mask)
+        with _on(dev, stream) as st:
+            dlogits = torch.empty((p.T, p.E), dtype=torch.float32, device=dev)
+            moe_route_backward(p, logits, ids, counts, dlogits, self.ws, grad_losses, grad_w,
+                               mask, st)
+        return dlogits
+
+    def _mask(self, what, mask):
+        if mask is None:
+            return None
+        if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _need(what, "mask", mask, torch.uint8, (self.p.T,), self.ws.device)
+        return mask
+
+    # -- layer norm -----------------------------------------------------------------------------
+    def _need_norm(self, what, x, *params):
+        p, dev = self.p, self.ws.device
+        _need(what, "x", x, self.torch_dtype, (p.T, p.d_model), dev)
+        for name, t in params:
+            _need(what, name, t, torch.float32, (p.d_model,), dev)
+
+    def layer_norm(self, x, gamma, beta, eps=1e-5, stream=None):
+        """(y, mean, rstd) of the layer norm of x [T, d_model]; gamma, beta [d_model] float32."""
+        p, dev = self.p, self.ws.device
+        self._need_norm("layer_norm", x, ("gamma", gamma), ("beta", beta))
+        with _on(dev, stream) as st:
+            y = torch.empty_like(x)
+            mean = torch.empty(p.T, dtype=torch.float32, device=dev)
+            rstd = torch.empty(p.T, dtype=torch.float32, device=dev)
+            moe_layer_norm(p, x, gamma, beta, eps, y, mean, rstd, st)
+        return y, mean, rstd
+
+    def layer_norm_backward(self, dy, x, gamma, mean, rstd, dres=None, stream=None):
+        """(dx, dgamma, dbeta) from dy and the forward's x, mean and rstd; ``dres`` [T, d_model]
+        (the residual's gradient) is added to dx."""
+        p, dev, what = self.p, self.ws.device, "layer_norm_backward"
+        self._need_norm(what, x, ("gamma", gamma))
+        for name, t in (("dy", dy), ("dres", dres)):
+            if name == "dy" or t is not None:
+                _need(what, name, t, self.torch_dtype, (p.T, p.d_model), dev)
+        _need(what, "mean", mean, torch.float32, (p.T,), dev)
+        _need(what, "rstd", rstd, torch.float32, (p.T,), dev)
+        with _on(dev, stream) as st:
+            dx = torch.empty_like(x)
+            dgamma = torch.empty(p.d_model, dtype=torch.float32, device=dev)
+            dbeta = torch.empty(p.d_model, dtype=torch.float32, device=dev)
+            moe_layer_norm_backward(p, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, self.ws, dres,
+                                    st)
+        return dx, dgamma, dbeta
+
+    # -- 4-bit expert weights -------------------------------------------------------------------
+    def _need_experts(self, what, W1, b1, W2, b2):
+        p, dev = self.p, self.ws.device
+        F1 = 2 * p.d_ff if p.flags & FLAG_GATED else p.d_ff
+        for name, W, shape in (("W1", W1, (p.E, F1, p.d_model)),
+                               ("W2", W2, (p.E, p.d_model, p.d_ff))):
+            if isinstance(W, W4Weights):
+                W._need(what, name, shape, dev)
+            else:
+                _need(what, name, W, self.torch_dtype, shape, dev)
+        for name, b, n in (("b1", b1, F1), ("b2", b2, p.d_model)):
+            if b is not None:
+                _need(what, name, b, torch.float32, (p.E, n), dev)
+
+    def expert_ffn_w4(self, x, offsets, rowtok, W1, b1, W2, b2, stream=None):
+        """:meth:`expert_ffn` over :class:`W4Weights`; the layer is made with ``w4=True``."""
+        p, dev, what = self.p, self.ws.device, "expert_ffn_w4"
+        if not (isinstance(W1, W4Weights) and isinstance(W2, W4Weights)):
+            raise MoeError(MOE_ERR_INVALID_ARG, what + ": W1 and W2 must be W4Weights")
+        _need(what, "x", x, torch.bfloat16, (p.T, p.d_model), dev)
+        _need(what, "offsets", offsets, torch.int32, (p.E + 1,), dev)
+        rows = rowtok.numel()
+        _need(what, "rowtok", rowtok, torch.int32, (max(self.max_rows, rows),), dev)
+        self._need_experts(what, W1, b1, W2, b2)
+        with _on(dev, stream) as st:
+            Y = torch.empty((max(self.max_rows, 1), p.d_model), dtype=x.dtype, device=dev)
+            moe_expert_ffn_packed(p, x, offsets, rowtok, W1.c, b1, W2.c, b2, Y, self.ws, st)
+        return Y
+
+    # -- the layer as a block of a model --------------------------------------------------------
+    def forward_block(self, x, Wr, br, W1, b1, W2, b2, norm=None, stream=None):
+        """The whole layer with an optional layer norm in front, ``norm`` = (gamma, beta, eps):
+        out = x + experts(norm(x)); W1 and W2 are tensors or both :class:`W4Weights`.  Returns
+        (out, routing and norm results: logits_out, ids_out, ..., and y, mean, rstd)."""
+        p, dev, what = self.p, self.ws.device, "forward_block"
+        w4 = isinstance(W1, W4Weights)
+        if w4 != isinstance(W2, W4Weights):
+            raise MoeError(MOE_ERR_INVALID_ARG, what + ": W1 and W2 must both be 4-bit or neither")
+        _need(what, "x", x, self.torch_dtype, (p.T, p.d_model), dev)
+        _need(what, "Wr", Wr, torch.float32, (p.d_model, p.E), dev)
+        if br is not None:
+            _need(what, "br", br, torch.float32, (p.E,), dev)
+        self._need_experts(what, W1, b1, W2, b2)
+        if norm is not None:
+            self._need_norm(what, x, ("gamma", norm[0]), ("beta", norm[1]))
+        with _on(dev, stream) as st:
+            def new(*shape, dtype=torch.float32):
+                return torch.empty(shape, dtype=dtype, device=dev)
+
+            out = torch.empty_like(x)
+            extra = dict(logits_out=new(p.T, p.E), ids_out=new(p.T, p.k, dtype=torch.int32),
+                         w_out=new(p.T, p.k), slot_out=new(p.T, p.k, dtype=torch.int32),
+                         drop_out=new(p.T, p.k, dtype=torch.uint8),
+                         counts_out=new(2 * p.E, dtype=torch.int32))
+            n, kept = None, {}
+            if norm is not None:
+                kept = dict(y=torch.empty_like(x), mean=new(p.T), rstd=new(p.T))
+                n = Norm(norm[0].data_ptr(), norm[1].data_ptr(), float(norm[2]),
+                         *(kept[key].data_ptr() for key in ("y", "mean", "rstd")))
+            moe_forward_block(p, x, n, Wr, br, None if w4 else W1, None if w4 else W2,
+                              W1.c if w4 else None, W2.c if w4 else None, b1, b2, out, self.ws,
+                              stream=st, **extra)
+        return out, {**extra, **kept}

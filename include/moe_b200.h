@@ -102,6 +102,32 @@ typedef struct {
  * or after the workspace was used for another problem; with stale terms the logits are wrong. */
 #define MOE_FLAG_ROUTER_PREPARED 8u
 
+/* 4-bit weights [E, N, K] with group scales (moe_quantize_packed makes them; any program may).
+ * Columns are cut into groups of `group` (32, 64 or 128; the last group of a row may be short).
+ *   q [E, N, 16 ceil(K / 128)] uint32: word 4 t + j of a row's 128-column chunk c holds columns
+ *     128 c + 32 j + 8 t + i, i = 0..7 (t, j in 0..3), column i as the nibble at bit
+ *     4 (4 (i % 2) + i / 2); columns past K hold 8.
+ *   scale, zero [E, ceil(K / group), N] bfloat16; zero may be NULL (no offsets).
+ * Value of column k of row n: scale * (nibble - 8) + zero, of group k / group.
+ * All three 16-byte aligned. */
+typedef struct {
+    const void* q;
+    const void* scale;
+    const void* zero;
+    int32_t group;
+} moe_w4;
+
+/* The layer norm in front of a block: parameters [d_model] float32, and where its output
+ * y [T, d_model] (x's dtype), mean and rstd [T] float32 go (kept for the backward pass). */
+typedef struct {
+    const float* gamma;
+    const float* beta;
+    float eps;
+    void* y;
+    float* mean;
+    float* rstd;
+} moe_norm;
+
 /* Host only.  Per-expert capacity K = min(T, floor(C * T * k / E)) evaluated in double
  * (worked example, capacity paragraph; generalised to k slots per token as in "Some Tokens Do
  * Not Get In").  Returns MOE_ERR_INVALID_ARG for a malformed problem. */
@@ -207,6 +233,93 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
                        void* out, float* logits_out, int32_t* ids_out, float* w_out,
                        int32_t* slot_out, uint8_t* drop_out, int32_t* counts_out, void* ws,
                        size_t ws_bytes, void* stream);
+
+/* ---- 4-bit expert weights ------------------------------------------------------------------
+ * Quantises W [E, N, K] (dtype MOE_BF16 or MOE_F32, dense, finite, 16-byte aligned) to the format
+ * of moe_w4.  Per group, zero = NULL: scale = max|w| / 7; else scale = (max - min) / 15 and zero =
+ * min + 8 scale.  Both are rounded to bfloat16 first (the divisions and sums in float32), then
+ * nibble - 8 = round-half-even((w - zero) / scale), clamped to [-8, 7]; 0 where scale = 0.
+ * K must be a multiple of 64 and N at most 2097120 (else MOE_ERR_UNSUPPORTED). */
+moe_status moe_quantize_packed(const void* W, int32_t dtype, int32_t E, int32_t N, int32_t K,
+                           int32_t group, void* q, void* scale, void* zero, void* stream);
+
+/* Reads 4-bit weights back: W [E, N, K] bfloat16, each value formed in float32 and rounded once.
+ * The same limits as moe_quantize_packed. */
+moe_status moe_dequantize_packed(const moe_w4* w, int32_t E, int32_t N, int32_t K, void* W,
+                             void* stream);
+
+/* Host only.  Workspace bytes for moe_expert_ffn_packed and moe_forward_block with 4-bit weights
+ * (at least moe_workspace_size, which suffices for the other calls). */
+moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes);
+
+/* moe_expert_ffn over 4-bit weights: W1 is [E, d_ff, d_model] ([E, 2 d_ff, d_model] with
+ * MOE_FLAG_GATED), W2 [E, d_model, d_ff]; their groups may differ.  p's dtype is MOE_BF16 (else
+ * MOE_ERR_UNSUPPORTED), with moe_expert_ffn's rules for widths, alignment, offsets and rowtok; rows
+ * of Y behind offsets[E] are left as they were.
+ * Few rows per expert (min(T k, E K) <= 96 E): the products read the 4-bit weights and form
+ * sum_k (nibble - 8) x_k per group exactly in float32 before the scale; b1, b2 nullable.  More rows:
+ * each weight is first read back to bfloat16 (one rounding per value) into the workspace, for the
+ * grouped tensor-core GEMM.  The hidden activations are kept in bfloat16 either way. */
+moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int32_t* offsets,
+                             const int32_t* rowtok, const moe_w4* W1, const float* b1,
+                             const moe_w4* W2, const float* b2, void* Y, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* ---- Layer norm ----------------------------------------------------------------------------
+ * y = gamma (x - mean) rstd + beta per token, rstd = 1 / sqrt(variance + eps), the variance over
+ * d_model without bias correction.  x, y [T, d_model] in p's dtype, any d_model; gamma, beta
+ * [d_model] float32; mean, rstd [T] float32 out.  eps >= 0 and finite.  y must not alias x.
+ * Statistics are float32, y is rounded once. */
+moe_status moe_layer_norm(const moe_problem* p, const void* x, const float* gamma,
+                          const float* beta, float eps, void* y, float* mean, float* rstd,
+                          void* stream);
+
+/* Its backward pass from dy, with the forward's x, mean and rstd: dx [T, d_model] in p's dtype,
+ * dgamma and dbeta [d_model] float32, written (not added to).  dres (nullable, [T, d_model], p's
+ * dtype) is added to dx before its one rounding: the gradient that reaches x past the norm, over
+ * the residual.  dx must not alias an input.  Results do not depend on scheduling. */
+moe_status moe_layer_norm_backward(const moe_problem* p, const void* dy, const void* x,
+                                   const float* gamma, const float* mean, const float* rstd,
+                                   const void* dres, void* dx, float* dgamma, float* dbeta,
+                                   void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Router training -----------------------------------------------------------------------
+ * Losses of a routing over the n tokens that mask [T] (nullable) leaves (0 leaves a token out;
+ * its logits and ids are not used and may hold anything).  With p_t = softmax(logits_t):
+ *   counts [E+1] int32: pairs (t, j) with ids[t k + j] = e, then n (before any capacity);
+ *   probs [E] float32: P_e = sum_t p_te / n;
+ *   losses [2] float32: E sum_e counts_e / (n k) P_e (load balance), sum_t lse_t^2 / n (z-loss,
+ *     lse_t = log sum_e exp logits_te).
+ * n = 0 gives zeros.  A token's logits hold at least one finite value, no NaN and no +infinity;
+ * -infinity is an expert it cannot take.  An id outside [0, E) is not counted and recorded as
+ * MOE_DEV_BAD_INDEX.  Results do not depend on scheduling. */
+moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int32_t* ids,
+                            const uint8_t* mask, float* losses, int32_t* counts, float* probs,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient with respect to the logits, dlogits [T, E] float32 (written; zero rows for tokens the
+ * mask leaves out):  of grad_losses[0] losses[0] + grad_losses[1] losses[1] (grad_losses [2]
+ * float32 on the device, with counts as moe_balance_loss gives them, or summed over the ranks of
+ * a group; NULL leaves this part out), plus that of the k routing weights w_tj, given their
+ * gradient grad_w [T k] float32 (NULL leaves it out; ids is read only with it, and is held
+ * constant).  MOE_FLAG_RENORMALIZE: the weights are the renormalised ones.  At least one of the
+ * two is given.  An id outside [0, E) is left out and recorded as MOE_DEV_BAD_INDEX; an id named
+ * twice by a token adds up.  dlogits must not alias logits. */
+moe_status moe_route_backward(const moe_problem* p, const float* logits, const int32_t* ids,
+                              const uint8_t* mask, const int32_t* counts,
+                              const float* grad_losses, const float* grad_w, float* dlogits,
+                              void* ws, size_t ws_bytes, void* stream);
+
+/* moe_forward as a block of a model: with norm (nullable) the router and the experts read
+ * norm(x) and the combine adds onto x, out = x + sum_j w_j FFN_j(norm(x)); with Q1 and Q2 (both,
+ * and W1 = W2 = NULL) the experts' weights are 4-bit, and ws_bytes must hold
+ * moe_workspace_size_packed.  Otherwise as moe_forward, bit for bit with neither. */
+moe_status moe_forward_block(const moe_problem* p, const void* x, const moe_norm* norm,
+                             const float* Wr, const float* br, const void* W1, const void* W2,
+                             const moe_w4* Q1, const moe_w4* Q2, const float* b1,
+                             const float* b2, void* out, float* logits_out, int32_t* ids_out,
+                             float* w_out, int32_t* slot_out, uint8_t* drop_out,
+                             int32_t* counts_out, void* ws, size_t ws_bytes, void* stream);
 
 /* Profiling aid, host only, per calling thread.  With n >= MOE_STAGE_EVENTS, moe_forward records
  * events[0..6] (cudaEvent_t handles owned by the caller) on its stream at: entry, after the
