@@ -35,6 +35,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "softmax.cuh"
+#include "tmap.h"
 
 namespace moe {
 
@@ -825,35 +826,6 @@ __global__ void __launch_bounds__(256) router_split_kernel(const float* __restri
 // ---------------------------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool encode_fn_ready() {
-    std::call_once(g_encode_once, []() {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    });
-    return g_encode != nullptr;
-}
-
-// 2-D bf16 tensor map over rows x cols (cols contiguous, row pitch `ld` elements).
-bool make_tmap_2d(CUtensorMap* tm, const void* ptr, long long rows, int cols, long long ld,
-                  int box_cols, int box_rows, CUtensorMapSwizzle swz) {
-    if (!encode_fn_ready()) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
 // Operand tile map: rows x K (K contiguous), box 64 x box_rows, 128-byte swizzle.
 bool make_tmap(CUtensorMap* tm, const void* ptr, long long rows, int K, int box_rows) {
     return make_tmap_2d(tm, ptr, rows, K, K, kBK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);

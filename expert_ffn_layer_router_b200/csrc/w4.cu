@@ -15,8 +15,11 @@
 #include <algorithm>
 #include <cstdint>
 
+#include <cuda.h>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "tmap.h"
 
 namespace moe {
 namespace {
@@ -144,14 +147,23 @@ __global__ void __launch_bounds__(256)
 }
 
 // The two columns of pair i (columns 2 i, 2 i + 1) of a word, as exact bfloat16 integers q - 8:
-// 0x4300 | q is 128 + q, and 136 is subtracted.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int i) {
-    const uint32_t u = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const uint32_t k136 = 0x43084308u;
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&k136));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
+// 0x4300 | q is 128 + q, and 136 is subtracted.  One lop3 needs both constants in registers;
+// `Unpack` holds them where the compiler cannot see their values (it splits the lop3 otherwise).
+struct Unpack {
+    uint32_t mask, magic;
+    __device__ __forceinline__ Unpack() {
+        asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(mask));
+        asm volatile("mov.b32 %0, 0x43004300;" : "=r"(magic));
+    }
+    __device__ __forceinline__ uint32_t pair(uint32_t word, int i) const {
+        uint32_t u;
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(u) : "r"(word >> (4 * i)), "r"(mask), "r"(magic));
+        const uint32_t k136 = 0x43084308u;
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&k136));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+};
 
 // Values in bfloat16, [E, N, K]: a thread per word (8 columns, one 16-byte store).
 __global__ void __launch_bounds__(256)
@@ -159,6 +171,7 @@ __global__ void __launch_bounds__(256)
                          const uint16_t* __restrict__ zero, int N, int K, int G,
                          long long words, uint16_t* __restrict__ W) {
     pdl_begin();
+    const Unpack unpack;
     const int C = (K + 127) / 128, groups = (K + G - 1) / G;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < words;
          i += (long long)gridDim.x * 256) {
@@ -172,7 +185,7 @@ __global__ void __launch_bounds__(256)
         uint32_t o[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const uint32_t v = w4_pair(word, p);
+            const uint32_t v = unpack.pair(word, p);
             o[p] = pack_bf16x2(fmaf(s, __uint_as_float(v << 16), z),
                                fmaf(s, __uint_as_float(v & 0xffff0000u), z));
         }
@@ -184,18 +197,24 @@ __global__ void __launch_bounds__(256)
 // The grouped products: D[r, n] = act(sum_k W[e]_nk A[row(r), k] + bias[e][n]) for the rows r of
 // each expert e.
 //
-// A unit is (expert, 32 * UG features, up to 32 rows); persistent blocks of 8 warps take equal
-// runs of the list of units.  Warp w works on 32 features (group w / KS) and every KS-th 128-column
-// chunk of K; the KS partial sums are added through shared memory in a fixed order at the end of
-// the unit.  Features are the M side of mma.m16n8k16 (weights as the A operand: lane (g, t) owns
-// features 4 g .. 4 g + 3 of the 32), rows the N side, so 8 rows cost one instruction per 16 x 16
-// weights.  The integers q - 8 are exact in bfloat16, so the products of a group are exact and
-// their fp32 sum is scaled once per group; offsets multiply the sum of x over the group, which an
-// all-ones operand gives.
+// A unit is (expert, 32 UG features, up to 32 / KS rows); one persistent block per SM, of 16 product
+// warps and two copying warps, takes an equal run of the list of units.  A step of a unit is KS
+// chunks of 128 columns (KS = 2, 4 or 8, UG = 16 / KS): warp w works on 32 features (w / KS) and on
+// chunk w % KS of the step; the KS sums are added through shared memory in a fixed order at the
+// unit's end.  Many units: KS = 2; few (one token): KS = 8 spreads K over the warps.
 //
-// Weights and scales come through a ring of cp.async stages private to each warp (each lane copies
-// the 16-byte pieces it uses itself), which runs ahead across units, so the stream of weights
-// never waits for the ends of units.
+// Features are the M side of mma.m16n8k16 (weights are the A operand: lane (g, t) owns features
+// g + 8 r, r < 4, of the 32), rows the N side, so 8 rows cost one instruction per 16 x 16 weights.
+// The integers q - 8 are exact in bfloat16, so a group's products are exact and their fp32 sum is
+// scaled once per group; offsets multiply the sum of x over the group, which an all-ones operand
+// gives.
+//
+// The copying warps fill a ring of stages that runs ahead across units: one the weights (tensor-map
+// copies of 128-byte rows: 64-byte rows took twice as long, the copy engine moves a row in about
+// 4 cycles), one scales and rows (16-byte cp.async: bulk copies are issued lane by lane, and 20 of
+// them took longer than a step's products).  Full / empty barriers hand the stages over.  Every wait
+// is bounded; one that runs out records MOE_DEV_TIMEOUT and the block finishes without waiting any
+// more.
 // ------------------------------------------------------------------------------------------------
 enum W4Epi { kW4SiLU = 0, kW4Bias = 1, kW4SwiGLU = 2 };
 
@@ -206,70 +225,70 @@ struct W4Args {
     const int32_t* offsets;   // [E + 1]
     int E, K, N;              // N: rows of W per expert (2 F when gated)
     int max_rows;
-    const uint32_t* q;
     const uint16_t* scale;
     const uint16_t* zero;     // nullable
-    int G;
     const float* bias;        // [E, N], nullable
     uint16_t* D;
     int ldd;
-    int ks;                   // warps that share a unit's K (1, 2, 4 or 8)
+    int lks;                  // log2 of KS, the warps that share a unit's K (2, 4 or 8)
     DeviceStatus* st;
 };
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;                         // product warps
+constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kStages = 4;
-constexpr int kRowTile = 32;                       // rows of a unit
-constexpr int kStageW = 2048;                      // weights of a stage: 32 features x 128 columns
-constexpr int kStageS = 256;                       // scales of a stage: 4 groups x 32 features
+constexpr int kLines = 16;                         // row pieces of a stage (rows x boxes)
+constexpr int kLineBytes = 512 + 64;               // 256 columns, padded: neighbours differ in bank
+constexpr int kStageX = kLines * kLineBytes;
+constexpr int kStageW = 256 * 128;                 // 32 UG features x KS chunks of 128 columns
 constexpr int kRedStride = 36;                     // floats per row of the partial sums
 constexpr int kRedBytes = kWarps * 8 * kRedStride * 4;
 
-template <bool ZERO>
-constexpr int kStageBytes = kStageW + (ZERO ? 2 : 1) * kStageS;
-template <bool ZERO>
+// A stage: weights (128-byte rows, 16-byte pieces swizzled by the row), rows, scales (and offsets).
+template <int G>
+constexpr int kSideBytes = 512 * (256 / G);
+template <bool ZERO, int G>
+constexpr int kStageBytes = kStageW + kStageX + (ZERO ? 2 : 1) * kSideBytes<G>;
+// (1024 bytes to align the ring; row pointers of the unit being copied; 2 flags)
+template <bool ZERO, int G>
 constexpr int w4_smem_bytes(int E) {
-    return kWarps * kStages * kStageBytes<ZERO> + 2 * kRedBytes + (E + 1) * 4;
-}
-
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
+    return 1024 + kStages * kStageBytes<ZERO, G> + kRedBytes + 2 * kStages * 8 + kLines * 8 +
+           (E + 2) * 4;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// d = a b (no accumulator to clear first).
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// 16 bytes to shared memory: copied (bytes = 16) or zeros (bytes = 0).
+__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
 
 // A unit's place: expert, feature block, first row of the row tile, rows in it.
 struct Unit { int e, fb, row0, rows; };
 
-template <int EPI, bool ZERO>
+template <int EPI, bool ZERO, int G>
 struct W4Kernel {
+    static constexpr int kPer = 256 / G;          // groups of a box
     const W4Args& a;
     const int* s_pre;         // units before each expert
-    int C, groups, UG, nfb;
-    int warp, lane, g, t, ug, ks;
+    int S, groups, nfb;       // 256-column boxes of K, groups of K, feature blocks
+    int UG, row_tile;         // 16 >> lks, 32 >> lks
 
     __device__ __forceinline__ Unit unit_at(int u) const {
         int lo = 0, hi = a.E - 1;                 // largest e with s_pre[e] <= u
@@ -278,104 +297,80 @@ struct W4Kernel {
             if (s_pre[mid] <= u) lo = mid; else hi = mid - 1;
         }
         const int r0 = a.offsets[lo], r1 = a.offsets[lo + 1];
-        const int tiles = (r1 - r0 + kRowTile - 1) / kRowTile;
+        const int tiles = (r1 - r0 + row_tile - 1) >> (5 - a.lks);
         const int i = u - s_pre[lo];
         Unit x;
         x.e = lo;
         x.fb = i / tiles;                         // row tiles of one feature block are neighbours:
-        x.row0 = r0 + (i - x.fb * tiles) * kRowTile;      // its weights are in the cache
-        x.rows = min(kRowTile, r1 - x.row0);
+        x.row0 = r0 + (i - x.fb * tiles) * row_tile;      // its weights are in the cache
+        x.rows = min(row_tile, r1 - x.row0);
         return x;
     }
-    // Row of W (within the expert) of this lane's first feature, and the step to the second pair:
-    // gated units hold 16 gate rows and the 16 up rows that go with them.
-    __device__ __forceinline__ int w_row(int fb) const {
-        const int f32 = fb * UG + ug;             // 32-feature block
-        return EPI == kW4SwiGLU ? f32 * 16 + 2 * g : f32 * 32 + 4 * g;
+    // First rows of W of the two halves of a unit's features (gated: gate rows, up rows).
+    __device__ __forceinline__ int first(const Unit& u, int h) const {
+        const int half = 16 * UG;
+        if constexpr (EPI == kW4SwiGLU) return h ? a.N / 2 + u.fb * half : u.fb * half;
+        return u.fb * 2 * half + h * half;
     }
-    __device__ __forceinline__ bool has_features(int fb) const {
-        return (fb * UG + ug) * 32 < a.N;
-    }
-    // Starts the copies of chunk c of unit x into the stage at `dst`.
-    __device__ __forceinline__ void fetch(uint32_t dst, const Unit& x, int c) const {
-        const int r = w_row(x.fb);
-        const long long words = 16LL * C;
-        const uint32_t* src = a.q + ((long long)x.e * a.N + r) * words + 16 * c + 4 * t;
-        const long long up = EPI == kW4SwiGLU ? (long long)(a.N / 2) * words : 2 * words;
-        cp_async_16(dst + lane * 16, src);
-        cp_async_16(dst + 512 + lane * 16, src + words);
-        cp_async_16(dst + 1024 + lane * 16, src + up);
-        cp_async_16(dst + 1536 + lane * 16, src + up + words);
-        const int gpc = 128 / a.G;
-        if (t < gpc) {
-            const int grp = c * gpc + t;
-            const bool in = grp < groups;
-            const long long at = ((long long)x.e * groups + (in ? grp : 0)) * a.N + r;
-            const uint32_t d = dst + kStageW + t * 64 + g * 8;
-            if constexpr (EPI == kW4SwiGLU) {
-                cp_async_4(d, a.scale + at, in ? 4 : 0);
-                cp_async_4(d + 4, a.scale + at + a.N / 2, in ? 4 : 0);
-                if constexpr (ZERO) {
-                    cp_async_4(d + kStageS, a.zero + at, in ? 4 : 0);
-                    cp_async_4(d + kStageS + 4, a.zero + at + a.N / 2, in ? 4 : 0);
-                }
-            } else {
-                cp_async_8(d, a.scale + at, in ? 8 : 0);
-                if constexpr (ZERO) cp_async_8(d + kStageS, a.zero + at, in ? 8 : 0);
-            }
-        }
-    }
-    // acc[nt][m] += chunk c's products for NT tiles of 8 rows.
+
+    // ---- product warps ----
+    // acc[n][m] += the products of this warp's chunk of a step for NT tiles of 8 rows; lane
+    // (g, t) of group ug: sums of features g + 16 m (+ 8) for rows 2 t, 2 t + 1 of tile n.
     template <int NT>
-    __device__ __forceinline__ void chunk(uint32_t stage, int c, const uint16_t* const (&xr)[4],
-                                          float (&acc)[4][2][4]) const {
+    __device__ __forceinline__ void chunk(const uint8_t* wl,
+                                          const uint8_t* sl, const uint8_t* xl,
+                                          const Unpack& unpack, float (&acc)[2][2][4]) const {
+        // r-th feature of the lane: 8 rows on, and 16 UG rows on between gate and up.
+        const int up = EPI == kW4SwiGLU ? 16 * UG : 16;
         uint4 w[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) w[r] = lds128(stage + r * 512 + lane * 16);
-        float part[NT][ZERO ? 3 : 2][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int m = 0; m < (ZERO ? 3 : 2); ++m)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[n][m][i] = 0.0f;
+        for (int r = 0; r < 4; ++r)
+            w[r] = *reinterpret_cast<const uint4*>(wl + ((r & 1) * 8 + (r >> 1) * up) * 128);
+        float part[NT][2][4], sum[NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint4 b[NT];
-            const int k = c * 128 + j * 32 + t * 8;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                b[n] = xr[n] && k < a.K ? *reinterpret_cast<const uint4*>(xr[n] + k)
-                                        : make_uint4(0, 0, 0, 0);
+            const bool first = j * 32 % G == 0;
             uint32_t p[4][4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const uint32_t word = j == 0 ? w[r].x : j == 1 ? w[r].y : j == 2 ? w[r].z : w[r].w;
+                const uint32_t word = j == 0 ? w[r].x : j == 1 ? w[r].y : j == 2 ? w[r].z
+                                                                                 : w[r].w;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[r][i] = w4_pair(word, i);
+                for (int i = 0; i < 4; ++i) p[r][i] = unpack.pair(word, i);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                const uint4 v =
+                    *reinterpret_cast<const uint4*>(xl + n * 8 * kLineBytes + j * 64);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const uint32_t a0[4] = {p[2 * m][0], p[2 * m + 1][0], p[2 * m][1],
                                             p[2 * m + 1][1]};
                     const uint32_t a1[4] = {p[2 * m][2], p[2 * m + 1][2], p[2 * m][3],
                                             p[2 * m + 1][3]};
-                    mma_bf16(part[n][m], a0, b[n].x, b[n].y);
-                    mma_bf16(part[n][m], a1, b[n].z, b[n].w);
+                    if (first) mma_bf16_first(part[n][m], a0, v.x, v.y);
+                    else mma_bf16(part[n][m], a0, v.x, v.y);
+                    mma_bf16(part[n][m], a1, v.z, v.w);
                 }
                 if constexpr (ZERO) {
-                    const uint32_t one[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-                    mma_bf16(part[n][2], one, b[n].x, b[n].y);
-                    mma_bf16(part[n][2], one, b[n].z, b[n].w);
+                    const uint32_t one[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u,
+                                             0x3f803f80u};
+                    if (first) mma_bf16_first(sum[n], one, v.x, v.y);
+                    else mma_bf16(sum[n], one, v.x, v.y);
+                    mma_bf16(sum[n], one, v.z, v.w);
                 }
             }
-            if (((j + 1) * 32) % a.G == 0) {
-                const int sg = j * 32 / a.G;
-                const uint2 s = lds64(stage + kStageW + sg * 64 + g * 8);
-                const float sc[4] = {bf16_bits(s.x & 0xffffu), bf16_bits(s.x >> 16),
-                                     bf16_bits(s.y & 0xffffu), bf16_bits(s.y >> 16)};
+            if ((j + 1) * 32 % G == 0) {
+                const uint8_t* s = sl + j * 32 / G * (64 * UG);
+                float sc[4], zo[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = ((r & 1) * 8 + (r >> 1) * up) * 2;
+                    sc[r] = bf16_bits(*reinterpret_cast<const uint16_t*>(s + at));
+                    if constexpr (ZERO)
+                        zo[r] = bf16_bits(*reinterpret_cast<const uint16_t*>(
+                            s + kSideBytes<G> + at));
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -383,51 +378,68 @@ struct W4Kernel {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             acc[n][m][i] = fmaf(sc[2 * m + i / 2], part[n][m][i], acc[n][m][i]);
-                            part[n][m][i] = 0.0f;
+                            if constexpr (ZERO)
+                                acc[n][m][i] = fmaf(zo[2 * m + i / 2], sum[n][i], acc[n][m][i]);
                         }
-                if constexpr (ZERO) {
-                    const uint2 zz = lds64(stage + kStageW + kStageS + sg * 64 + g * 8);
-                    const float zo[4] = {bf16_bits(zz.x & 0xffffu), bf16_bits(zz.x >> 16),
-                                         bf16_bits(zz.y & 0xffffu), bf16_bits(zz.y >> 16)};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                acc[n][m][i] = fmaf(zo[2 * m + i / 2], part[n][2][i], acc[n][m][i]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) part[n][2][i] = 0.0f;
-                    }
-                }
             }
+        }
+    }
+    // Bias, activation and the store of one row's sums: v[r] of feature g + 8 r of 32-feature
+    // block b (gated: gate g, gate g + 8, up g, up g + 8 of 16).
+    __device__ __forceinline__ void store(const Unit& x, int b, int g, int row,
+                                          const float (&sums)[4]) const {
+        uint16_t* out = a.D + (long long)(x.row0 + row) * a.ldd;
+        const float* bias = a.bias ? a.bias + (long long)x.e * a.N : nullptr;
+        const int f = (EPI == kW4SwiGLU ? b * 16 : b * 32) + g;
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int n = EPI == kW4SwiGLU ? f + 8 * (r & 1) + (r >> 1) * (a.N / 2) : f + 8 * r;
+            v[r] = sums[r] + (bias ? bias[n] : 0.0f);
+        }
+        if constexpr (EPI == kW4SwiGLU) {
+            out[f] = bf16_round(silu(v[0]) * v[2]);
+            out[f + 8] = bf16_round(silu(v[1]) * v[3]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) out[f + 8 * r] = bf16_round(EPI == kW4SiLU ? silu(v[r]) : v[r]);
         }
     }
 };
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
-
-template <int EPI, bool ZERO>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_gemm_kernel(const W4Args args) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* red = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes<ZERO>);
-    int* s_pre = reinterpret_cast<int*>(smem + kWarps * kStages * kStageBytes<ZERO> +
-                                        2 * kRedBytes);
-    W4Kernel<EPI, ZERO> w{args, s_pre};
-    w.C = (args.K + 127) / 128;
-    w.groups = (args.K + args.G - 1) / args.G;
-    w.UG = kWarps / args.ks;
-    w.nfb = (args.N / 32 + w.UG - 1) / w.UG;
-    w.warp = threadIdx.x >> 5;
-    w.lane = threadIdx.x & 31;
-    w.g = w.lane >> 2;
-    w.t = w.lane & 3;
-    w.ug = w.warp / args.ks;
-    w.ks = w.warp % args.ks;
-    const int E = args.E, lane = w.lane;
+template <int EPI, bool ZERO, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    w4_gemm_kernel(const __grid_constant__ CUtensorMap tm, const W4Args args) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    constexpr int kStage = kStageBytes<ZERO, G>;
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float* red = reinterpret_cast<float*>(smem + kStages * kStage);
+    const uint32_t bars = smem_u32(red) + kRedBytes;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (kStages + s); };
+    const uint16_t** s_row = reinterpret_cast<const uint16_t**>(
+        reinterpret_cast<uint8_t*>(red) + kRedBytes + 2 * kStages * 8);
+    int* s_pre = reinterpret_cast<int*>(s_row + kLines);
+    int* s_bad = s_pre + args.E + 1;
+    W4Kernel<EPI, ZERO, G> w{args, s_pre};
+    const int KS = 1 << args.lks, NB = KS / 2;       // chunks and 256-column boxes of a step
+    w.S = (args.K + 255) / 256;
+    w.groups = (args.K + G - 1) / G;
+    w.UG = kWarps >> args.lks;
+    w.nfb = (args.N / 32 + w.UG - 1) >> (4 - args.lks);
+    w.row_tile = 2 * kLines >> args.lks;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = args.E;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full_bar(s), 1 + 32);      // the weights' bytes; each lane's own copies
+            mbar_init(empty_bar(s), kWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
+    }
     pdl_begin();
-    __shared__ int s_bad;
-    if (w.warp == 0) {
+    if (warp == 0) {
         // Units before each expert; offsets are checked as the grouped GEMM does: 0 first,
         // non-decreasing, at most max_rows.  Bad offsets: nothing is computed or stored.
         int total = 0;
@@ -439,7 +451,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_gemm_kernel(const W4Args ar
             int n = e < E ? args.offsets[e + 1] - args.offsets[e] : 0;
             bad |= n < 0;
             n = max(n, 0);
-            const int units = (n + kRowTile - 1) / kRowTile * w.nfb;
+            const int units = ((n + w.row_tile - 1) >> (5 - args.lks)) * w.nfb;
             int inc = units;
 #pragma unroll
             for (int h = 1; h < 32; h *= 2) {
@@ -452,130 +464,219 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_gemm_kernel(const W4Args ar
         bad = __any_sync(kFull, bad);
         if (lane == 0) {
             s_pre[E] = total;
-            s_bad = bad;
+            *s_bad = bad;
             if (bad && blockIdx.x == 0) report(args.st, MOE_DEV_BAD_INDEX, 710);
         }
     }
     __syncthreads();
-    if (s_bad) return;
+    if (*s_bad) return;
     const int total = s_pre[E];
     const int u0 = (int)((long long)total * blockIdx.x / gridDim.x);
     const int u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
-    if (u0 >= u1) return;
 
-    const uint32_t ring = smem_u32(smem) + w.warp * kStages * kStageBytes<ZERO>;
-    // The fetcher walks (unit, chunk) ahead of the products.
-    int fu = u0, fc = w.ks, fslot = 0;
-    Unit fx = w.unit_at(u0);
-    auto fetch_next = [&]() {
-        if (fu < u1) {
-            // (no features, or no chunk of this warp: units of nothing to fetch are skipped)
-            while (fu < u1 && (fc >= w.C || !w.has_features(fx.fb))) {
-                fc = w.ks;
-                if (++fu < u1) fx = w.unit_at(fu);
+    if (warp == kWarps) {
+        // ---- copies the weights ----
+        if (lane == 0) {
+            int slot = 0;
+            uint32_t phase = 0, issued = 0;
+            const int half = 16 * w.UG;
+            bool ok = true;
+            for (int u = u0; u < u1 && ok; ++u) {
+                const Unit x = w.unit_at(u);
+                const int r0 = x.e * args.N + w.first(x, 0), r1 = x.e * args.N + w.first(x, 1);
+                for (int c = 0; c < w.S; c += NB) {
+                    ok = mbar_wait(empty_bar(slot), phase ^ 1u, args.st, 71);
+                    if (!ok) break;
+                    // (features past the end: rows of the next expert, not used)
+                    const int boxes = min(NB, w.S - c);
+                    uint32_t dst = smem_u32(smem) + slot * kStage;
+                    mbar_arrive_expect_tx(full_bar(slot), (uint32_t)(boxes * 2 * half * 128));
+                    for (int q = 0; q < boxes; ++q, dst += 2 * half * 128) {
+                        tma_load_2d(dst, &tm, full_bar(slot), (c + q) * 64, r0);
+                        tma_load_2d(dst + half * 128, &tm, full_bar(slot), (c + q) * 64, r1);
+                    }
+                    ++issued;
+                    if (++slot == kStages) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
             }
-            if (fu < u1) {
-                w.fetch(ring + fslot * kStageBytes<ZERO>, fx, fc);
-                fslot = fslot + 1 == kStages ? 0 : fslot + 1;
-                fc += args.ks;
+            // The last copies must land before the block's shared memory goes away, also when a
+            // wait gave up and the product warps no longer wait for them (bounded again).
+            for (uint32_t i = issued - min(issued, (uint32_t)kStages); i < issued; ++i) {
+                const uint64_t t0 = global_ns();
+                while (!mbar_try_wait(full_bar(i % kStages), (i / kStages) & 1u) &&
+                       global_ns() - t0 < kWaitLimitNs) {}
+            }
+        }
+        return;
+    }
+    if (warp == kWarps + 1) {
+        // ---- copies scales and rows: lane l the 16-byte piece l of every line of rows ----
+        int slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok; ++u) {
+            const Unit x = w.unit_at(u);
+            // Rows of the lines (box line / row_tile, row line % row_tile; null: no row).
+            const bool two = args.lks > 1 || x.rows > 8;      // (else lines 8 .. 15 are not read)
+            __syncwarp();
+            if (lane < kLines) {
+                const int rr = lane & (w.row_tile - 1);
+                const uint16_t* src = nullptr;
+                if (rr < x.rows) {
+                    int r = x.row0 + rr;
+                    if (args.a_rows) {
+                        r = args.a_rows[r];
+                        if (r < 0 || r >= args.a_row_limit) {
+                            report(args.st, MOE_DEV_BAD_INDEX, 720);
+                            r = -1;
+                        }
+                    }
+                    if (r >= 0)
+                        src = args.A + (long long)r * args.K + (lane >> (5 - args.lks)) * 256;
+                }
+                s_row[lane] = src;
+            }
+            __syncwarp();
+            // The lane's piece of each line; a line without a row is never copied (zeros).
+            const uint16_t* line[kLines];
+            uint32_t there = 0;
+#pragma unroll
+            for (int i = 0; i < kLines; ++i) {
+                const uint16_t* src = s_row[i];
+                there |= (src != nullptr ? 1u : 0u) << i;
+                line[i] = src ? src + lane * 8 : args.A;
+            }
+            // Scales: piece i of the lane belongs to group i NB + lg of the step; 8 features from
+            // f (past the end: none).
+            const int lg = lane >> (6 - args.lks), piece = lane & (4 * w.UG - 1);
+            const int f = w.first(x, piece >= 2 * w.UG) + (piece & (2 * w.UG - 1)) * 8;
+            const long long per_step = (long long)NB * args.N;
+            long long side = ((long long)x.e * w.groups + lg) * args.N + f;
+            int left = f < args.N ? w.groups - lg : 0;       // groups from this lane's first on
+            int cols = args.K - lane * 8;                    // columns from this lane's piece on
+            for (int c = 0; c < w.S; c += NB, cols -= NB * 256) {
+                ok = __all_sync(kFull, mbar_wait(empty_bar(slot), phase ^ 1u, args.st, 73));
+                if (!ok) break;
+                const uint32_t dst = smem_u32(smem) + slot * kStage + kStageW + lane * 16;
+#pragma unroll
+                for (int i = 0; i < kLines; ++i) {
+                    if (i == 8 && !two) break;
+                    const bool in = ((there >> i) & 1u) && cols > (i >> (5 - args.lks)) * 256;
+                    cp_async_16z(dst + i * kLineBytes, line[i], in ? 16 : 0);
+                    if (cols > NB * 256) line[i] += NB * 256;    // (stays inside the row)
+                }
+#pragma unroll
+                for (int i = 0; i < W4Kernel<EPI, ZERO, G>::kPer; ++i) {
+                    const bool in = left > 0;
+                    const uint32_t d = dst + kStageX + 32 * i * 16;
+                    cp_async_16z(d, args.scale + (in ? side : 0), in ? 16 : 0);
+                    if constexpr (ZERO)
+                        cp_async_16z(d + kSideBytes<G>, args.zero + (in ? side : 0), in ? 16 : 0);
+                    side += per_step;
+                    left -= NB;
+                }
+                cp_async_arrive_noinc(full_bar(slot));
+                if (++slot == kStages) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
             }
         }
         cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch_next();
+        cp_async_wait<0>();
+        return;
+    }
 
-    int slot = 0, buf = 0;
+    const int g = lane >> 2, t = lane & 3, ug = warp >> args.lks, ks = warp & (KS - 1);
+    const Unpack unpack;
+    // This lane's places in a stage: first feature's words, its scale, its row of the first tile.
+    // (With KS > 4 a box has fewer than 8 rows; lanes of the columns past them read other lines, or
+    // what lies behind the last one: their sums are not used.)
+    const int box = ks >> 1, h = ks & 1;
+    const int frow = EPI == kW4SwiGLU ? ug * 16 + g : ug * 32 + g;
+    const int w_at = (box * 32 * w.UG + frow) * 128 + (((h * 4 + t) ^ g) << 4);
+    const int x_at = kStageW + (box * w.row_tile + g) * kLineBytes + h * 256 + t * 16;
+    const int s_at = kStageW + kStageX + (box * (256 / G) + h * (128 / G)) * 64 * w.UG + frow * 2;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
     for (int u = u0; u < u1; ++u) {
         const Unit x = w.unit_at(u);
         const int nt = (x.rows + 7) / 8;
-        const uint16_t* xr[4];
+        const int bl = x.fb * w.UG + ug;
+        const bool feat = bl * 32 < args.N;
+        float acc[2][2][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int r = n * 8 + w.g;
-            xr[n] = nullptr;
-            if (r < x.rows) {
-                int src = x.row0 + r;
-                if (args.a_rows) {
-                    src = args.a_rows[src];
-                    if (src < 0 || src >= args.a_row_limit) {
-                        report(args.st, MOE_DEV_BAD_INDEX, 720);
-                        src = -1;
-                    }
-                }
-                if (src >= 0) xr[n] = args.A + (long long)src * args.K;
-            }
-        }
-        float acc[4][2][4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.0f;
-        if (w.has_features(x.fb)) {
-            for (int c = w.ks; c < w.C; c += args.ks) {
-                fetch_next();
-                cp_async_wait<kStages - 1>();
-                __syncwarp();          // scales were copied by other lanes of the warp
-                const uint32_t stage = ring + slot * kStageBytes<ZERO>;
-                if (nt == 1) w.template chunk<1>(stage, c, xr, acc);
-                else if (nt == 2) w.template chunk<2>(stage, c, xr, acc);
-                else w.template chunk<4>(stage, c, xr, acc);
-                __syncwarp();          // before the stage is filled again
-                slot = slot + 1 == kStages ? 0 : slot + 1;
+#pragma unroll 1
+        for (int c = 0; c < w.S; c += NB) {
+            if (ok) ok = __all_sync(kFull, mbar_wait(full_bar(slot), phase, args.st, 72));
+            if (ok && feat && (c + box) * 256 + h * 128 < args.K) {
+                const uint8_t* stage = smem + slot * kStage;
+                if (nt == 1)
+                    w.template chunk<1>(stage + w_at, stage + s_at, stage + x_at, unpack, acc);
+                else
+                    w.template chunk<2>(stage + w_at, stage + s_at, stage + x_at, unpack, acc);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_bar(slot));
+            if (++slot == kStages) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
-        // Join the KS partial sums, 8 rows at a time, and store.
+        // acc[n][m][i]: row 2 t + i % 2 of tile n, feature g + 16 m + 8 (i / 2).
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n < nt) {
-                float* rb = red + buf * (kRedBytes / 4);
-                float* mine = rb + (w.warp * 8 + 2 * w.t) * kRedStride + 4 * w.g;
-                // rows 2t, 2t + 1; features 4g .. 4g + 3 = (m0 lo, m0 hi, m1 lo, m1 hi)
-                *reinterpret_cast<float4*>(mine) = make_float4(acc[n][0][0], acc[n][0][2],
-                                                               acc[n][1][0], acc[n][1][2]);
-                *reinterpret_cast<float4*>(mine + kRedStride) =
-                    make_float4(acc[n][0][1], acc[n][0][3], acc[n][1][1], acc[n][1][3]);
-                __syncthreads();
-                constexpr int kOut = EPI == kW4SwiGLU ? 16 : 32;      // features per 32 rows of W
-                for (int i = threadIdx.x; i < w.UG * 8 * kOut; i += kWarps * 32) {
-                    const int ug = i / (8 * kOut), row = i / kOut % 8, f = i % kOut;
-                    const int f32 = x.fb * w.UG + ug;
-                    if (n * 8 + row >= x.rows || f32 * 32 >= args.N) continue;
-                    // Gated: features 2 g, 2 g + 1 of the 16 are columns 4 g, 4 g + 1 (gate) and
-                    // 4 g + 2, 4 g + 3 (up) of the sums.
-                    const int col = EPI == kW4SwiGLU ? 4 * (f >> 1) + (f & 1) : f;
-                    const float* s = rb + (ug * args.ks * 8 + row) * kRedStride + col;
-                    float v = 0.0f, up = 0.0f;
-                    for (int q = 0; q < args.ks; ++q) {
-                        v += s[q * 8 * kRedStride];
-                        if (EPI == kW4SwiGLU) up += s[q * 8 * kRedStride + 2];
-                    }
-                    const int feat = f32 * kOut + f;
-                    if (args.bias) {
-                        const float* b = args.bias + (long long)x.e * args.N;
-                        v += b[feat];
-                        if (EPI == kW4SwiGLU) up += b[args.N / 2 + feat];
-                    }
-                    if (EPI == kW4SiLU) v = silu(v);
-                    if (EPI == kW4SwiGLU) v = silu(v) * up;
-                    args.D[(long long)(x.row0 + n * 8 + row) * args.ldd + feat] = bf16_round(v);
-                }
-                buf ^= 1;
+        for (int n = 0; n < 2; ++n) {
+            if (n >= nt) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float* mine = red + (warp * 8 + 2 * t + i) * kRedStride + g;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mine[8 * q] = acc[n][q >> 1][i + 2 * (q & 1)];
             }
+            asm volatile("bar.sync 1, 512;" ::: "memory");
+            // Thread i < 64 UG joins 4 features of a row: (group, row, g).
+            const int i = threadIdx.x, jg = i >> 6, row = (i >> 3) & 7, fg = i & 7;
+            const int jb = x.fb * w.UG + jg;
+            if (ok && jg < w.UG && n * 8 + row < x.rows && jb * 32 < args.N) {
+                const float* s = red + ((jg << args.lks) * 8 + row) * kRedStride + fg;
+                float v[4] = {s[0], s[8], s[16], s[24]};
+                for (int q = 1; q < KS; ++q)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] += s[q * 8 * kRedStride + 8 * r];
+                w.store(x, jb, fg, n * 8 + row, v);
+            }
+            asm volatile("bar.sync 1, 512;" ::: "memory");
         }
     }
-    cp_async_wait<0>();
 }
 
-template <int EPI, bool ZERO>
-cudaError_t run_w4(const W4Args& a, cudaStream_t s) {
-    auto kern = w4_gemm_kernel<EPI, ZERO>;
-    const int smem = w4_smem_bytes<ZERO>(a.E);
+template <int EPI, bool ZERO, int G>
+cudaError_t run_w4(const CUtensorMap& tm, const W4Args& a, cudaStream_t s) {
+    auto kern = w4_gemm_kernel<EPI, ZERO, G>;
+    const int smem = w4_smem_bytes<ZERO, G>(a.E);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (note_launch(e) != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(2 * kSm), dim3(kWarps * 32), smem, s, a);
+    return launch_pdl(kern, dim3(kSm), dim3(kThreads), smem, s, tm, a);
+}
+
+template <int EPI>
+cudaError_t run_w4(const CUtensorMap& tm, const W4Args& a, int G, cudaStream_t s) {
+    if (a.zero)
+        return G == 32   ? run_w4<EPI, true, 32>(tm, a, s)
+               : G == 64 ? run_w4<EPI, true, 64>(tm, a, s)
+                         : run_w4<EPI, true, 128>(tm, a, s);
+    return G == 32   ? run_w4<EPI, false, 32>(tm, a, s)
+           : G == 64 ? run_w4<EPI, false, 64>(tm, a, s)
+                     : run_w4<EPI, false, 128>(tm, a, s);
 }
 
 }  // namespace
@@ -618,14 +719,25 @@ cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int 
                            const uint32_t* q, const uint16_t* scale, const uint16_t* zero, int G,
                            const float* bias, void* D, int ldd, DeviceStatus* st, cudaStream_t s,
                            int* launches) {
-    W4Args a{(const uint16_t*)A, a_rows, a_row_limit, offsets, E, K, N, max_rows, q, scale, zero,
-             G, bias, (uint16_t*)D, ldd, 8, st};
-    // Warps that share a unit's K: as many as there are chunks, at most 8.
-    while (a.ks > 1 && a.ks > (K + 127) / 128) a.ks /= 2;
+    W4Args a{(const uint16_t*)A, a_rows, a_row_limit, offsets, E, K, N, max_rows, scale, zero,
+             bias, (uint16_t*)D, ldd, 1, st};
+    // Warps that share a unit's K: the fewest that give every block a unit, at most 8 and no more
+    // than there are chunks.  (One token, 8 experts of 2048 x 1024: 26, 22 and 20 us for KS = 2, 4
+    // and 8, and 27 for 16, whose rows fill 2 of the 8 columns of an instruction; 64 tokens, all
+    // experts: 74, 86 and 166 us.)
+    while (a.lks < 3 && (256 << a.lks) <= K &&
+           (long long)std::min(E, max_rows) * (N / 32) < (long long)kSm * (kWarps >> a.lks))
+        a.lks += 1;
+    // Words as 16-bit pairs: boxes of 128 bytes (256 columns) x 16 UG rows.
+    const int cols = 32 * ((K + 127) / 128);
+    CUtensorMap tm;
+    if (!make_tmap_2d(&tm, q, (long long)E * N, cols, cols, 64, 16 * (kWarps >> a.lks),
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+        return note_launch(cudaErrorInvalidValue);
     cudaError_t e;
-    if (which == kW4SiLU) e = zero ? run_w4<kW4SiLU, true>(a, s) : run_w4<kW4SiLU, false>(a, s);
-    else if (which == kW4Bias) e = zero ? run_w4<kW4Bias, true>(a, s) : run_w4<kW4Bias, false>(a, s);
-    else e = zero ? run_w4<kW4SwiGLU, true>(a, s) : run_w4<kW4SwiGLU, false>(a, s);
+    if (which == kW4SiLU) e = run_w4<kW4SiLU>(tm, a, G, s);
+    else if (which == kW4Bias) e = run_w4<kW4Bias>(tm, a, G, s);
+    else e = run_w4<kW4SwiGLU>(tm, a, G, s);
     *launches += 1;
     return e;
 }

@@ -7,7 +7,6 @@ There is no CPU path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -213,6 +212,15 @@ def moe_forward(p, x, Wr, br, W1, b1, W2, b2, out, ws, logits_out=None, ids_out=
            "moe_forward")
 
 
+def _at(t):
+    """A tensor's address as a plain int (None stays None)."""
+    return None if t is None else t.data_ptr()
+
+
+def _at_stream(stream):
+    return stream if isinstance(stream, int) else _stream(stream)
+
+
 def moe_workspace_size_packed(p: Problem) -> int:
     n = ctypes.c_size_t()
     _check(_lib.moe_workspace_size_packed(ctypes.byref(p), ctypes.byref(n)), "moe_workspace_size_packed")
@@ -221,13 +229,13 @@ def moe_workspace_size_packed(p: Problem) -> int:
 
 def moe_quantize_packed(W, E, N, K, group, q, scale, zero=None, stream=None):
     dtype = MOE_BF16 if W.dtype == torch.bfloat16 else MOE_F32
-    _check(_lib.moe_quantize_packed(_ptr(W), dtype, int(E), int(N), int(K), int(group), _ptr(q),
-                                _ptr(scale), _ptr(zero), _stream(stream)), "moe_quantize_packed")
+    _check(_lib.moe_quantize_packed(_at(W), dtype, int(E), int(N), int(K), int(group), _at(q),
+                                _at(scale), _at(zero), _at_stream(stream)), "moe_quantize_packed")
 
 
 def moe_dequantize_packed(w: W4, E, N, K, W, stream=None):
-    _check(_lib.moe_dequantize_packed(ctypes.byref(w), int(E), int(N), int(K), _ptr(W),
-                                  _stream(stream)), "moe_dequantize_packed")
+    _check(_lib.moe_dequantize_packed(ctypes.byref(w), int(E), int(N), int(K), _at(W),
+                                  _at_stream(stream)), "moe_dequantize_packed")
 
 
 def _ref(s):
@@ -235,50 +243,50 @@ def _ref(s):
 
 
 def moe_expert_ffn_packed(p, x, offsets, rowtok, W1: W4, b1, W2: W4, b2, Y, ws, stream=None):
-    _check(_lib.moe_expert_ffn_packed(ctypes.byref(p), _ptr(x), _ptr(offsets), _ptr(rowtok),
-                                  _ref(W1), _ptr(b1), _ref(W2), _ptr(b2), _ptr(Y), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)),
+    _check(_lib.moe_expert_ffn_packed(ctypes.byref(p), _at(x), _at(offsets), _at(rowtok),
+                                  _ref(W1), _at(b1), _ref(W2), _at(b2), _at(Y), _at(ws),
+                                  ws.numel() * ws.element_size(), _at_stream(stream)),
            "moe_expert_ffn_packed")
 
 
 def moe_layer_norm(p, x, gamma, beta, eps, y, mean, rstd, stream=None):
-    _check(_lib.moe_layer_norm(ctypes.byref(p), _ptr(x), _ptr(gamma), _ptr(beta), float(eps),
-                               _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream)),
+    _check(_lib.moe_layer_norm(ctypes.byref(p), _at(x), _at(gamma), _at(beta), float(eps),
+                               _at(y), _at(mean), _at(rstd), _at_stream(stream)),
            "moe_layer_norm")
 
 
 def moe_layer_norm_backward(p, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, ws, dres=None,
                             stream=None):
-    _check(_lib.moe_layer_norm_backward(ctypes.byref(p), _ptr(dy), _ptr(x), _ptr(gamma),
-                                        _ptr(mean), _ptr(rstd), _ptr(dres), _ptr(dx),
-                                        _ptr(dgamma), _ptr(dbeta), _ptr(ws),
-                                        ws.numel() * ws.element_size(), _stream(stream)),
+    _check(_lib.moe_layer_norm_backward(ctypes.byref(p), _at(dy), _at(x), _at(gamma),
+                                        _at(mean), _at(rstd), _at(dres), _at(dx),
+                                        _at(dgamma), _at(dbeta), _at(ws),
+                                        ws.numel() * ws.element_size(), _at_stream(stream)),
            "moe_layer_norm_backward")
 
 
 def moe_balance_loss(p, logits, ids, losses, counts, probs, ws, mask=None, stream=None):
-    _check(_lib.moe_balance_loss(ctypes.byref(p), _ptr(logits), _ptr(ids), _ptr(mask),
-                                 _ptr(losses), _ptr(counts), _ptr(probs), _ptr(ws),
-                                 ws.numel() * ws.element_size(), _stream(stream)),
+    _check(_lib.moe_balance_loss(ctypes.byref(p), _at(logits), _at(ids), _at(mask),
+                                 _at(losses), _at(counts), _at(probs), _at(ws),
+                                 ws.numel() * ws.element_size(), _at_stream(stream)),
            "moe_balance_loss")
 
 
 def moe_route_backward(p, logits, ids, counts, dlogits, ws, grad_losses=None, grad_w=None,
                        mask=None, stream=None):
-    _check(_lib.moe_route_backward(ctypes.byref(p), _ptr(logits), _ptr(ids), _ptr(mask),
-                                   _ptr(counts), _ptr(grad_losses), _ptr(grad_w), _ptr(dlogits),
-                                   _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+    _check(_lib.moe_route_backward(ctypes.byref(p), _at(logits), _at(ids), _at(mask),
+                                   _at(counts), _at(grad_losses), _at(grad_w), _at(dlogits),
+                                   _at(ws), ws.numel() * ws.element_size(), _at_stream(stream)),
            "moe_route_backward")
 
 
 def moe_forward_block(p, x, norm, Wr, br, W1, W2, Q1, Q2, b1, b2, out, ws, logits_out=None,
                       ids_out=None, w_out=None, slot_out=None, drop_out=None, counts_out=None,
                       stream=None):
-    _check(_lib.moe_forward_block(ctypes.byref(p), _ptr(x), _ref(norm), _ptr(Wr), _ptr(br),
-                                  _ptr(W1), _ptr(W2), _ref(Q1), _ref(Q2), _ptr(b1), _ptr(b2),
-                                  _ptr(out), _ptr(logits_out), _ptr(ids_out), _ptr(w_out),
-                                  _ptr(slot_out), _ptr(drop_out), _ptr(counts_out), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)),
+    _check(_lib.moe_forward_block(ctypes.byref(p), _at(x), _ref(norm), _at(Wr), _at(br),
+                                  _at(W1), _at(W2), _ref(Q1), _ref(Q2), _at(b1), _at(b2),
+                                  _at(out), _at(logits_out), _at(ids_out), _at(w_out),
+                                  _at(slot_out), _at(drop_out), _at(counts_out), _at(ws),
+                                  ws.numel() * ws.element_size(), _at_stream(stream)),
            "moe_forward_block")
 
 
@@ -320,25 +328,42 @@ def moe_set_stage_events(events):
 # Argument checks and streams of the tensor-level calls below
 # ----------------------------------------------------------------------------------------------
 def _need(what, name, t, dtype, shape, device):
-    """``t`` must be a dense tensor of this type and shape on ``device``."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or
+    """``t`` must be a dense tensor of this type and shape (a tuple) on ``device``."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or
             t.device != device or not t.is_contiguous()):
         raise MoeError(MOE_ERR_INVALID_ARG, "%s: %s must be a contiguous %s tensor of shape %s on %s"
                        % (what, name, dtype, tuple(shape), device))
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _on:
     """Makes ``device`` and ``stream`` (None: the device's current stream) current, so results
-    allocated inside belong to the stream that writes them; yields the stream."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device)
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            with torch.cuda.stream(stream):
-                yield stream
+    allocated inside belong to the stream that writes them; gives the stream's handle.  Entering
+    with the current device and no stream, the usual case, changes nothing."""
+
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, ()
+
+    def __enter__(self):
+        index = self.device.index
+        if self.stream is None and index == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(index)
+        guards = [torch.cuda.device(self.device)]
+        guards[0].__enter__()
+        if self.stream is not None:
+            st = self.stream
+            if not hasattr(st, "cuda_stream"):
+                st = torch.cuda.ExternalStream(int(st), device=self.device)
+            guards.append(torch.cuda.stream(st))
+            guards[1].__enter__()
+        self.guards = guards
+        return torch._C._cuda_getCurrentRawStream(index)
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
 
 
 class W4Weights:
