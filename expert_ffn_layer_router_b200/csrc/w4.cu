@@ -14,6 +14,7 @@
 // the bytes of W: each is read once, half a byte.  See w4_gemm_kernel.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -38,33 +39,33 @@ __device__ __forceinline__ uint16_t bf16_round(float v) {
 // 15) and z = bf16(min + 8 s).  q - 8 = round-half-even((w - z) / s) clamped to [-8, 7], 0 where
 // s = 0.  The rounding of s and z to bfloat16 (they are what is kept) comes before the division,
 // so it costs at most half a step more.
+//
+// The quotients.  With i = 1 / s rounded once and t = w i, the corrected t + (w - t s) i (two fused
+// steps) is the correctly rounded quotient (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990), so halves are met exactly; where s is so small that its
+// reciprocal or the remainder leaves the normal range, a thread divides.  Adding 1.5 * 2^23 + 8
+// rounds t half to even and leaves q in the low bits; the eight words of bits are joined as
+// acc = 16 acc + bits modulo 2^32, and the constant's share is taken off at the end.
+// (64 x 1024 x 2048 from bfloat16, 0.34 GB moved: with a division near halves 143 us, half of the
+// warps meeting one.)
 // ------------------------------------------------------------------------------------------------
-
-// rint(a / s) as the IEEE quotient rounds, without a division unless the quotient is near a half:
-// a * (1 / s) is within 2^-22 relative of it, and |quotient| < 16 where it matters.
-__device__ __forceinline__ float quotient_rint(float a, float s, float inv) {
-    float t = a * inv;
-    const float f = t - truncf(t);
-    if (fabsf(fabsf(f) - 0.5f) < 1e-4f || !(fabsf(t) < 64.0f)) t = __fdiv_rn(a, s);
-    return rintf(t);
-}
+constexpr float kRound = 12582920.0f;                  // 1.5 * 2^23 + 8 (even: halves stay halves)
+constexpr uint32_t kRoundBits = 0x4b400008u - 8u;      // its bits, without the 8
 
 template <class T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&f)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack8(const uint4 (&raw)[sizeof(T) / 2], float (&f)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(u[i] << 16);
-        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int q = 0; q < (int)sizeof(T) / 2; ++q) {
+        const uint32_t u[4] = {raw[q].x, raw[q].y, raw[q].z, raw[q].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                f[2 * i] = __uint_as_float(u[i] << 16);
+                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            } else {
+                f[4 * q + i] = __uint_as_float(u[i]);
+            }
+        }
     }
 }
 
@@ -73,75 +74,113 @@ __device__ __forceinline__ void load8<uint16_t>(const uint16_t* p, float (&f)[8]
 // 64-byte runs.
 constexpr int kQRows = 32, kQChunks = 4;
 
-template <class T>
+// Bits of a nibble: column i of a word sits at 4 (4 (i % 2) + i / 2).
+__device__ __forceinline__ constexpr int column_at(int nibble) {
+    return nibble < 4 ? 2 * nibble : 2 * (nibble - 4) + 1;
+}
+
+template <class T, bool ZERO, int G>
 __global__ void __launch_bounds__(256)
-    w4_quantize_kernel(const T* __restrict__ W, int N, int K, int G, int row_tiles,
+    w4_quantize_kernel(const T* __restrict__ W, int N, int K, int row_tiles,
                        uint32_t* __restrict__ q, uint16_t* __restrict__ scale,
                        uint16_t* __restrict__ zero) {
     pdl_begin();
-    __shared__ uint16_t s_scale[kQChunks * 4][kQRows], s_zero[kQChunks * 4][kQRows];
-    const int e = blockIdx.y / row_tiles, n0 = (blockIdx.y % row_tiles) * kQRows;
+    constexpr int kPer = 128 / G, kLanes = G / 8;
+    __shared__ uint16_t s_scale[kQChunks * kPer][kQRows], s_zero[kQChunks * kPer][kQRows];
+    const int e = blockIdx.y / row_tiles, n0 = (blockIdx.y - e * row_tiles) * kQRows;
     const int chunk0 = blockIdx.x * kQChunks, C = (K + 127) / 128;
     const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
-    const int lanes = G / 8, gpc = 128 / G;             // lanes per group, groups per chunk
+    const int c = chunk0 + half % kQChunks, k = c * 128 + l * 8;
     const float kInf = __int_as_float(0x7f800000);
-#pragma unroll 2
-    for (int it = half; it < kQRows * kQChunks; it += 16) {
-        const int c = chunk0 + it % kQChunks, r = it / kQChunks, n = n0 + r;
-        const int k = c * 128 + l * 8;
-        const bool in = n < N && k < K;                 // K is a multiple of 64
-        float v[8];
-        if (in) {
-            load8<T>(W + ((long long)e * N + n) * K + k, v);
-        } else {
+    const T* src = W + ((long long)e * N + n0) * K + k;
+    uint32_t* dst = q + ((long long)e * N + n0) * (16LL * C) + 16 * c + 4 * (l & 3) + (l >> 2);
+    // (16 half-warps: 4 rows a step, 8 steps, the loads of kAhead of them in flight together)
+    constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;
+#pragma unroll 1
+    for (int step = 0; step < 8; step += kAhead) {
+        uint4 raw[kAhead][sizeof(T) / 2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        }
-        float lo = kInf, hi = -kInf;
-        if (in) {
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = half / kQChunks + 4 * (step + i);
+            const bool in = n0 + r < N && k < K;            // K is a multiple of 64
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                lo = fminf(lo, v[i]);
-                hi = fmaxf(hi, v[i]);
-            }
+            for (int p = 0; p < (int)sizeof(T) / 2; ++p)
+                raw[i][p] = in ? reinterpret_cast<const uint4*>(src + (long long)r * K)[p]
+                               : make_uint4(0, 0, 0, 0);
         }
-        for (int h = 1; h < lanes; h *= 2) {
-            lo = fminf(lo, __shfl_xor_sync(kFull, lo, h));
-            hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, h));
-        }
-        uint16_t sb = 0, zb = 0;
-        if (hi >= lo) {
-            if (zero) {
-                sb = bf16_round(__fdiv_rn(__fsub_rn(hi, lo), 15.0f));
-                zb = bf16_round(__fadd_rn(lo, __fmul_rn(8.0f, bf16_bits(sb))));
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = half / kQChunks + 4 * (step + i);
+            const bool in = n0 + r < N && k < K;
+            float v[8];
+            unpack8<T>(raw[i], v);
+            // (a group that lies past K or N gives scale 0 and is not stored; the columns of a group
+            // are all in or all out up to 64, and zeros past K inside a group of 128 change only the
+            // extremes with offsets)
+            float s, z = 0.0f;
+            if constexpr (ZERO) {
+                float lo = in ? v[0] : kInf, hi = in ? v[0] : -kInf;
+#pragma unroll
+                for (int i = 1; i < 8; ++i) {
+                    lo = fminf(lo, in ? v[i] : kInf);
+                    hi = fmaxf(hi, in ? v[i] : -kInf);
+                }
+#pragma unroll
+                for (int h = 1; h < kLanes; h *= 2) {
+                    lo = fminf(lo, __shfl_xor_sync(kFull, lo, h));
+                    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, h));
+                }
+                const bool any = hi >= lo;
+                s = any ? bf16_bits(bf16_round(__fdiv_rn(__fsub_rn(hi, lo), 15.0f))) : 0.0f;
+                z = any ? bf16_bits(bf16_round(__fadd_rn(lo, __fmul_rn(8.0f, s)))) : 0.0f;
             } else {
-                sb = bf16_round(__fdiv_rn(fmaxf(hi, -lo), 7.0f));
-            }
-        }
-        const float s = bf16_bits(sb), z = bf16_bits(zb), inv = 1.0f / s;
-        uint32_t word = 0;
+                float top = fabsf(v[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float t = 0.0f;
-            if (in && s > 0.0f)
-                t = fminf(fmaxf(quotient_rint(__fsub_rn(v[i], z), s, inv), -8.0f), 7.0f);
-            word |= (uint32_t)((int)t + 8) << (4 * (4 * (i & 1) + i / 2));
-        }
-        if (n < N && c < C)
-            q[((long long)e * N + n) * (16LL * C) + 16 * c + 4 * (l & 3) + (l >> 2)] = word;
-        if (l % lanes == 0) {
-            s_scale[(it % kQChunks) * gpc + l / lanes][r] = sb;
-            s_zero[(it % kQChunks) * gpc + l / lanes][r] = zb;
+                for (int i = 1; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+                for (int h = 1; h < kLanes; h *= 2)
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, h));
+                s = bf16_bits(bf16_round(__fdiv_rn(top, 7.0f)));
+            }
+            const float inv = __frcp_rn(s);
+            uint32_t acc = 0;
+#pragma unroll
+            for (int b = 7; b >= 0; --b) {                  // nibble b, from the highest
+                const float w = ZERO ? __fsub_rn(v[column_at(b)], z) : v[column_at(b)];
+                float t = __fmul_rn(w, inv);
+                t = __fmaf_rn(__fmaf_rn(-t, s, w), inv, t);
+                if constexpr (ZERO) t = fminf(fmaxf(t, -8.0f), 7.0f);
+                acc = acc * 16u + __float_as_uint(__fadd_rn(t, kRound));
+            }
+            uint32_t word = acc - kRoundBits * 0x11111111u;
+            // (without offsets |t| stays below 7.1 for such s, so nothing has to be clamped)
+            if (!(s > 7.9e-31f)) {
+                word = 0;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    const float w = ZERO ? __fsub_rn(v[column_at(b)], z) : v[column_at(b)];
+                    const float t = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(w, s)), -8.0f), 7.0f) : 0.0f;
+                    word |= (uint32_t)((int)t + 8) << (4 * b);
+                }
+            }
+            if (!in) word = 0x88888888u;
+            if (n0 + r < N && c < C) dst[(long long)r * 16 * C] = word;
+            if (l % kLanes == 0) {
+                s_scale[half % kQChunks * kPer + l / kLanes][r] = (uint16_t)(__float_as_uint(s) >> 16);
+                if (ZERO)
+                    s_zero[half % kQChunks * kPer + l / kLanes][r] =
+                        (uint16_t)(__float_as_uint(z) >> 16);
+            }
         }
     }
     __syncthreads();
     const int groups = (K + G - 1) / G;
-    for (int i = threadIdx.x; i < kQChunks * gpc * kQRows; i += 256) {
-        const int g = chunk0 * gpc + i / kQRows, n = n0 + i % kQRows;
+    for (int i = threadIdx.x; i < kQChunks * kPer * kQRows; i += 256) {
+        const int g = chunk0 * kPer + i / kQRows, n = n0 + i % kQRows;
         if (g < groups && n < N) {
             const long long o = ((long long)e * groups + g) * N + n;
             scale[o] = s_scale[i / kQRows][i % kQRows];
-            if (zero) zero[o] = s_zero[i / kQRows][i % kQRows];
+            if (ZERO) zero[o] = s_zero[i / kQRows][i % kQRows];
         }
     }
 }
@@ -165,31 +204,65 @@ struct Unpack {
     }
 };
 
-// Values in bfloat16, [E, N, K]: a thread per word (8 columns, one 16-byte store).
+// Values in bfloat16, [E, N, K], on the quantiser's tiles: a lane per word (8 columns, one 16-byte
+// store; 16 lanes write 256 bytes in a row).  Without offsets the product s (q - 8) is exact in
+// 12 bits, so the bfloat16 multiply rounds it once, like the float32 one.
+template <bool ZERO, int G>
 __global__ void __launch_bounds__(256)
     w4_dequantize_kernel(const uint32_t* __restrict__ q, const uint16_t* __restrict__ scale,
-                         const uint16_t* __restrict__ zero, int N, int K, int G,
-                         long long words, uint16_t* __restrict__ W) {
+                         const uint16_t* __restrict__ zero, int N, int K, int row_tiles,
+                         uint16_t* __restrict__ W) {
     pdl_begin();
+    constexpr int kPer = 128 / G;
+    __shared__ uint16_t s_scale[kQChunks * kPer][kQRows], s_zero[kQChunks * kPer][kQRows];
+    const int e = blockIdx.y / row_tiles, n0 = (blockIdx.y - e * row_tiles) * kQRows;
+    const int chunk0 = blockIdx.x * kQChunks, C = (K + 127) / 128, groups = (K + G - 1) / G;
     const Unpack unpack;
-    const int C = (K + 127) / 128, groups = (K + G - 1) / G;
-    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < words;
-         i += (long long)gridDim.x * 256) {
-        const long long row = i / (16 * C);
-        const int w = (int)(i - row * (16 * C));
-        const int k = (w >> 4) * 128 + (w & 3) * 32 + ((w >> 2) & 3) * 8;
-        if (k >= K) continue;
-        const uint32_t word = q[i];
-        const long long e = row / N, at = (e * groups + k / G) * N + (row - e * N);
-        const float s = bf16_bits(scale[at]), z = zero ? bf16_bits(zero[at]) : 0.0f;
-        uint32_t o[4];
+    const int half = threadIdx.x >> 4, l = threadIdx.x & 15, cc = half % kQChunks;
+    const int c = chunk0 + cc;
+    const uint32_t* src = q + ((long long)e * N + n0) * (16LL * C) + 16 * c + l;
+    uint32_t word[kQRows / 4];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t v = unpack.pair(word, p);
-            o[p] = pack_bf16x2(fmaf(s, __uint_as_float(v << 16), z),
-                               fmaf(s, __uint_as_float(v & 0xffff0000u), z));
+    for (int i = 0; i < kQRows / 4; ++i) {
+        const int r = half / kQChunks + 4 * i;
+        word[i] = n0 + r < N && c < C ? src[(long long)r * 16 * C] : 0;
+    }
+    for (int i = threadIdx.x; i < kQChunks * kPer * kQRows; i += 256) {
+        const int g = chunk0 * kPer + i / kQRows, n = n0 + i % kQRows;
+        const bool in = g < groups && n < N;
+        const long long o = in ? ((long long)e * groups + g) * N + n : 0;
+        s_scale[i / kQRows][i % kQRows] = in ? scale[o] : 0;
+        if (ZERO) s_zero[i / kQRows][i % kQRows] = in ? zero[o] : 0;
+    }
+    __syncthreads();
+    const int kk = (l & 3) * 32 + (l >> 2) * 8, k = c * 128 + kk;
+    if (k >= K) return;
+    uint16_t* dst = W + ((long long)e * N + n0) * K + k;
+#pragma unroll
+    for (int i = 0; i < kQRows / 4; ++i) {
+        const int r = half / kQChunks + 4 * i;
+        if (n0 + r >= N) break;
+        const uint16_t sb = s_scale[cc * kPer + kk / G][r];
+        uint32_t o[4];
+        if constexpr (ZERO) {
+            const float s = bf16_bits(sb), z = bf16_bits(s_zero[cc * kPer + kk / G][r]);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t v = unpack.pair(word[i], p);
+                o[p] = pack_bf16x2(fmaf(s, __uint_as_float(v << 16), z),
+                                   fmaf(s, __uint_as_float(v & 0xffff0000u), z));
+            }
+        } else {
+            const uint32_t s2 = sb * 0x10001u;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t v = unpack.pair(word[i], p);
+                const __nv_bfloat162 r2 = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                                  *reinterpret_cast<const __nv_bfloat162*>(&s2));
+                o[p] = *reinterpret_cast<const uint32_t*>(&r2);
+            }
         }
-        *reinterpret_cast<uint4*>(W + row * K + k) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + (long long)r * K) = make_uint4(o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -681,37 +754,70 @@ cudaError_t run_w4(const CUtensorMap& tm, const W4Args& a, int G, cudaStream_t s
 
 }  // namespace
 
-void launch_w4_quantize(int dtype, const void* W, int E, int N, int K, int G, uint32_t* q,
-                        uint16_t* scale, uint16_t* zero, cudaStream_t s, int* launches) {
-    const int row_tiles = (N + kQRows - 1) / kQRows;
-    const int C = (K + 127) / 128;
-    // Row tiles of all experts on y (at most 65535 a launch), chunks on x.
-    const int per = 65535 / row_tiles > 0 ? 65535 / row_tiles : 1;
-    const int groups = (K + G - 1) / G;
+namespace {
+
+// Calls f(first expert, experts, grid) for the tiles of E experts: row tiles on y (at most 65535 a
+// launch), chunks on x.
+template <class F>
+void w4_tiles(int E, int N, int K, F f) {
+    const int row_tiles = (N + kQRows - 1) / kQRows, C = (K + 127) / 128;
+    const int per = 65535 / row_tiles;
     for (int e0 = 0; e0 < E; e0 += per) {
         const int ne = std::min(per, E - e0);
-        const dim3 grid((C + kQChunks - 1) / kQChunks, ne * row_tiles);
-        const long long rows = (long long)e0 * N;
-        uint16_t* z = zero ? zero + rows * groups : nullptr;
-        if (dtype == MOE_BF16)
-            launch_pdl(w4_quantize_kernel<uint16_t>, grid, dim3(256), 0, s,
-                       (const uint16_t*)W + rows * K, N, K, G, row_tiles, q + rows * 16 * C,
-                       scale + rows * groups, z);
-        else
-            launch_pdl(w4_quantize_kernel<float>, grid, dim3(256), 0, s,
-                       (const float*)W + rows * K, N, K, G, row_tiles, q + rows * 16 * C,
-                       scale + rows * groups, z);
-        *launches += 1;
+        f(e0, row_tiles, dim3((C + kQChunks - 1) / kQChunks, ne * row_tiles));
     }
+}
+
+// f(bool constant, group constant)
+template <class F>
+void w4_format(bool zero, int G, F f) {
+    auto with = [&](auto z) {
+        if (G == 32) f(z, std::integral_constant<int, 32>());
+        else if (G == 64) f(z, std::integral_constant<int, 64>());
+        else f(z, std::integral_constant<int, 128>());
+    };
+    if (zero) with(std::true_type());
+    else with(std::false_type());
+}
+
+}  // namespace
+
+void launch_w4_quantize(int dtype, const void* W, int E, int N, int K, int G, uint32_t* q,
+                        uint16_t* scale, uint16_t* zero, cudaStream_t s, int* launches) {
+    const long long words = 16LL * ((K + 127) / 128), groups = (K + G - 1) / G;
+    w4_tiles(E, N, K, [&](int e0, int row_tiles, dim3 grid) {
+        const long long rows = (long long)e0 * N;
+        w4_format(zero != nullptr, G, [&](auto z, auto g) {
+            constexpr bool Z = decltype(z)::value;
+            constexpr int kG = decltype(g)::value;
+            uint16_t* zp = Z ? zero + rows * groups : nullptr;
+            if (dtype == MOE_BF16)
+                launch_pdl(w4_quantize_kernel<uint16_t, Z, kG>, grid, dim3(256), 0, s,
+                           (const uint16_t*)W + rows * K, N, K, row_tiles, q + rows * words,
+                           scale + rows * groups, zp);
+            else
+                launch_pdl(w4_quantize_kernel<float, Z, kG>, grid, dim3(256), 0, s,
+                           (const float*)W + rows * K, N, K, row_tiles, q + rows * words,
+                           scale + rows * groups, zp);
+        });
+        *launches += 1;
+    });
 }
 
 void launch_w4_dequantize(const uint32_t* q, const uint16_t* scale, const uint16_t* zero, int E,
                           int N, int K, int G, void* W, cudaStream_t s, int* launches) {
-    const long long words = (long long)E * N * 16 * ((K + 127) / 128);
-    const int blocks = (int)std::min<long long>((words + 255) / 256, kSm * 32);
-    launch_pdl(w4_dequantize_kernel, dim3(blocks), dim3(256), 0, s, q, scale, zero, N, K, G, words,
-               (uint16_t*)W);
-    *launches += 1;
+    const long long words = 16LL * ((K + 127) / 128), groups = (K + G - 1) / G;
+    w4_tiles(E, N, K, [&](int e0, int row_tiles, dim3 grid) {
+        const long long rows = (long long)e0 * N;
+        w4_format(zero != nullptr, G, [&](auto z, auto g) {
+            constexpr bool Z = decltype(z)::value;
+            launch_pdl(w4_dequantize_kernel<Z, decltype(g)::value>, grid, dim3(256), 0, s,
+                       q + rows * words, scale + rows * groups,
+                       Z ? zero + rows * groups : (const uint16_t*)nullptr, N, K, row_tiles,
+                       (uint16_t*)W + rows * K);
+        });
+        *launches += 1;
+    });
 }
 
 cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int a_row_limit,
