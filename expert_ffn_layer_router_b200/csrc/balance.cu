@@ -26,7 +26,7 @@ namespace moe {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMaxCluster = 8;
+constexpr uint32_t kMaxCluster = 8;
 constexpr int kMaxClusters = 36;    // two blocks on (almost) every SM
 
 // Block size: 4 NV values, as many sums and the loads in flight have to fit the registers.
@@ -149,7 +149,7 @@ __device__ __forceinline__ void write_losses(int E, int k, int n, float zsum, Cn
 // words per cluster).
 // part = null: the only cluster, which writes the results itself.
 template <int G, int NV, bool VEC>
-__global__ void __launch_bounds__(kThreadsOf<NV>)
+__global__ void __launch_bounds__(kThreadsOf<NV>, 2)
     balance_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                    const uint8_t* __restrict__ mask, int T, int E, int k, int rows_per_block,
                    float* __restrict__ part, float* losses, int32_t* counts, float* probs,
@@ -172,10 +172,11 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
     for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
     __syncthreads();
     // Pair counts of the block's tokens.
-    for (int i = threadIdx.x; i < (t1 - t0) * k; i += kThreads) {
-        const int t = t0 + i / k;
-        if (!mask || mask[t]) {
-            const int e = ids[(long long)t0 * k + i];
+    for (int t = t0 + threadIdx.x; t < t1; t += kThreads) {
+        if (mask && !mask[t]) continue;
+#pragma unroll 8
+        for (int j = 0; j < k; ++j) {
+            const int e = ids[(long long)t * k + j];
             if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
             else report(st, MOE_DEV_BAD_INDEX, 610);
         }
@@ -186,12 +187,20 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
     float z = 0.0f;
     float n = 0.0f;
     // Every group of a warp makes the same number of steps (the shuffles name the whole warp).
+    // The next row's logits are loaded before this one's sums.
     const int steps = (t1 - t0 + kGroups - 1) / kGroups;
+    int t = t0 + threadIdx.x / G;
+    bool coming = t < t1 && (!mask || mask[t]);
+    float next[4 * NV];
+    load_row<G, NV, VEC>(logits + (long long)t * E, E, l, coming, next);
     for (int i = 0; i < steps; ++i) {
-        const int t = t0 + i * kGroups + threadIdx.x / G;
-        const bool live = t < t1 && (!mask || mask[t]);
+        const bool live = coming;
         float v[4 * NV];
-        load_row<G, NV, VEC>(logits + (long long)t * E, E, l, live, v);
+#pragma unroll
+        for (int q = 0; q < 4 * NV; ++q) v[q] = next[q];
+        t += kGroups;
+        coming = t < t1 && (!mask || mask[t]);
+        load_row<G, NV, VEC>(logits + (long long)t * E, E, l, coming, next);
         const float2 ms = softmax_terms<G, NV>(v, live);
         const float r = 1.0f / ms.y;
 #pragma unroll
@@ -226,22 +235,29 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
     if (size > 1) cluster_sync(); else __syncthreads();
     if (rank == 0) {
         const uint32_t a_p = smem_u32(s_p), a_c = smem_u32(s_cnt), a_z = smem_u32(s_z);
-        auto psum = [&](int e) {
-            float v = 0.0f;
-            for (uint32_t r = 0; r < size; ++r) v += ld_cluster_f32(map_rank(a_p + 4 * e, r));
+        // (all ranks' words in flight together, added in rank order)
+        auto psum_at = [&](uint32_t a) {
+            float f[kMaxCluster], v = 0.0f;
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r)
+                f[r] = r < size ? ld_cluster_f32(map_rank(a, r)) : 0.0f;
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r) v += f[r];
             return v;
         };
-        auto cnt = [&](int e) {
-            int v = 0;
-            for (uint32_t r = 0; r < size; ++r) v += ld_cluster_s32(map_rank(a_c + 4 * e, r));
+        auto cnt_at = [&](uint32_t a) {
+            int f[kMaxCluster], v = 0;
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r)
+                f[r] = r < size ? ld_cluster_s32(map_rank(a, r)) : 0;
+#pragma unroll
+            for (uint32_t r = 0; r < kMaxCluster; ++r) v += f[r];
             return v;
         };
-        float zs = 0.0f;
-        int ns = 0;
-        for (uint32_t r = 0; r < size; ++r) {
-            zs += ld_cluster_f32(map_rank(a_z, r));
-            ns += ld_cluster_s32(map_rank(a_z + 4, r));
-        }
+        auto psum = [&](int e) { return psum_at(a_p + 4 * e); };
+        auto cnt = [&](int e) { return cnt_at(a_c + 4 * e); };
+        const float zs = psum_at(a_z);
+        const int ns = cnt_at(a_z + 4);
         if (part) {
             float* o = part + (long long)(blockIdx.x / size) * 2 * (E + 1);
             int* oc = reinterpret_cast<int*>(o + E + 1);
@@ -260,26 +276,40 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
     if (size > 1) cluster_sync();      // the peers' shared memory stays until rank 0 has read it
 }
 
+// Joins the clusters' totals (one block): thread (g, c) adds column c of clusters g, g + groups, ...,
+// whose loads are all in flight together, and the groups' sums are added in order.
 __global__ void __launch_bounds__(1024)
     balance_final_kernel(const float* __restrict__ part, int nc, int E, int k, float* losses,
                          int32_t* counts, float* probs) {
     pdl_begin();
     __shared__ float s_buf[32];
-    const long long stride = 2 * (E + 1);
+    extern __shared__ float s_part[];                         // [groups][cols], then row 0 the totals
+    const int cols = 2 * (E + 1);                             // floats, then ints from E + 1 on
+    const int groups = cols > 1024 ? 1 : 1024 / cols;
     const int* ipart = reinterpret_cast<const int*>(part);
-    auto psum = [&](int e) {
-        float v = 0.0f;
-#pragma unroll 6
-        for (int c = 0; c < nc; ++c) v += part[c * stride + e];
-        return v;
-    };
-    auto cnt = [&](int e) {
-        int v = 0;
-#pragma unroll 6
-        for (int c = 0; c < nc; ++c) v += ipart[c * stride + E + 1 + e];
-        return v;
-    };
-    write_losses(E, k, cnt(E), psum(E), cnt, psum, losses, counts, probs, s_buf);
+    int* s_ipart = reinterpret_cast<int*>(s_part);
+    const int g = groups == 1 ? 0 : threadIdx.x / cols;
+    for (int c = threadIdx.x - g * cols; c < cols && g < groups; c += 1024) {
+        float f = 0.0f;
+        int n = 0;
+#pragma unroll 12
+        for (int i = g; i < nc; i += groups) {
+            if (c <= E) f += part[(long long)i * cols + c];
+            else n += ipart[(long long)i * cols + c];
+        }
+        if (c <= E) s_part[g * cols + c] = f;
+        else s_ipart[g * cols + c] = n;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < cols; c += 1024) {
+        for (int i = 1; i < groups; ++i) {
+            if (c <= E) s_part[c] += s_part[i * cols + c];
+            else s_ipart[c] += s_ipart[i * cols + c];
+        }
+    }
+    __syncthreads();
+    write_losses(E, k, s_ipart[E + 1 + E], s_part[E], [&](int e) { return s_ipart[E + 1 + e]; },
+                 [&](int e) { return s_part[e]; }, losses, counts, probs, s_buf);
 }
 
 template <int G, int NV, bool VEC>
@@ -293,7 +323,6 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
     constexpr int kGroups = kThreadsOf<NV> / G;
     const int lane = threadIdx.x & 31;
     const int l = lane & (G - 1);
-    const unsigned gmask = (G == 32 ? kFull : ((1u << (G & 31)) - 1u)) << (lane & ~(G - 1));
     // a_e without the routing weights' part, per lane; counts[E] = 0 only if no token is left.
     float base[4 * NV];
     float gz = 0.0f, scale = 0.0f;
@@ -307,82 +336,108 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
         const int e = expert_of<G, VEC>(l, i);
         base[i] = grad_losses && e < E ? scale * (float)counts[e] : 0.0f;
     }
+    // grad_w: the group's row of dw' (zeros between tokens) and of the lanes that own its entries.
+    extern __shared__ float s_rows[];
+    float* row = s_rows + (threadIdx.x / G) * E;
+    uint8_t* own = reinterpret_cast<uint8_t*>(s_rows + kGroups * E) + (threadIdx.x / G) * E;
+    if (grad_w) {
+        for (int e = l; e < E; e += G) row[e] = 0.0f;
+        __syncwarp();
+    }
     const long long all = (long long)gridDim.x * kGroups;
     const long long steps = (T + all - 1) / all;
+    long long t = (long long)blockIdx.x * kGroups + threadIdx.x / G;
+    // What a step reads of memory is loaded during the step before.
+    float next[4 * NV];
+    bool coming;
+    int next_id = -1;
+    float next_dw = 0.0f;
+    auto fetch = [&]() {
+        coming = t < T && (!mask || mask[t]);
+        load_row<G, NV, VEC>(logits + t * E, E, l, coming, next);
+        if (grad_w) {
+            next_id = coming && l < k ? ids[t * k + l] : -1;
+            next_dw = coming && l < k ? grad_w[t * k + l] : 0.0f;
+        }
+    };
+    fetch();
     for (long long i = 0; i < steps; ++i) {
-        const long long t = i * all + (long long)blockIdx.x * kGroups + threadIdx.x / G;
-        const bool in = t < T;
-        const bool live = in && (!mask || mask[t]);
+        const long long at = t;
+        const bool in = at < T, live = coming;
         float v[4 * NV];
-        load_row<G, NV, VEC>(logits + t * E, E, l, live, v);
+#pragma unroll
+        for (int q = 0; q < 4 * NV; ++q) v[q] = next[q];
+        int id = next_id;
+        float dw = next_dw;
+        t += all;
+        fetch();
         const float2 ms = softmax_terms<G, NV>(v, live);
         const float r = 1.0f / ms.y;
-        float dot = 0.0f;
+        float a[4 * NV];
 #pragma unroll
-        for (int q = 0; q < 4 * NV; ++q) {
-            v[q] *= r;
-            dot = fmaf(v[q], base[q], dot);
-        }
-        // Lane j < k of the group holds pair j: its expert, p and dw'.
-        int id = -1 - l;
-        float pj = 0.0f, dw = 0.0f;
+        for (int q = 0; q < 4 * NV; ++q) a[q] = base[q];
         if (grad_w) {
-            if (live && l < k) {
-                id = ids[t * k + l];
-                if (id >= 0 && id < E) {
-                    pj = expf(logits[t * E + id] - ms.x) * r;
-                    dw = grad_w[t * k + l];
-                } else {
-                    report(st, MOE_DEV_BAD_INDEX, 620);
-                    id = -1 - l;
-                }
+            // Lane j < k of the group holds pair j: its expert and dw'.
+            if (live && l < k && (id < 0 || id >= E)) {
+                report(st, MOE_DEV_BAD_INDEX, 620);
+                id = -1;
+                dw = 0.0f;
             }
             if (renorm) {
+                const float pj = id >= 0 ? expf(logits[at * E + id] - ms.x) * r : 0.0f;
                 const float S = group_sum<G>(pj);
                 const float d = group_sum<G>(dw * pj);
                 dw = S > 0.0f ? (dw - d / S) / S : 0.0f;
             }
-            dot += pj * dw;
+            // An expert named twice: the lane that did not win its entry sees another's number
+            // there, and its pairs' dw' are added up (in pair order) in every lane that names it.
+            if (id >= 0) own[id] = (uint8_t)l;
+            __syncwarp();
+            if (__any_sync(kFull, id >= 0 && own[id] != l)) {
+                float sum = 0.0f;
+                for (int j = 0; j < G; ++j) {
+                    const int oid = __shfl_sync(kFull, id, j, G);
+                    const float o = __shfl_sync(kFull, dw, j, G);
+                    if (oid == id) sum += o;
+                }
+                dw = sum;
+            }
+            if (id >= 0) row[id] = dw;
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4 * NV; ++q) {
+                const int e = expert_of<G, VEC>(l, q);
+                if (e < E) a[q] += row[e];
+            }
+            __syncwarp();
+            if (id >= 0) row[id] = 0.0f;
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4 * NV; ++q) {
+            v[q] *= r;
+            dot = fmaf(v[q], a[q], dot);
         }
         dot = group_sum<G>(dot);
         const float shift = live ? gz * (ms.x + logf(ms.y)) - dot : 0.0f;
         if (in) {
-            float* out = dlogits + t * E;
+            float* out = dlogits + at * E;
             if constexpr (VEC) {
 #pragma unroll
                 for (int q = 0; q < NV; ++q) {
                     const int e = 4 * (l + G * q);
                     if (e < E)
                         *reinterpret_cast<float4*>(out + e) = make_float4(
-                            v[4 * q] * (base[4 * q] + shift),
-                            v[4 * q + 1] * (base[4 * q + 1] + shift),
-                            v[4 * q + 2] * (base[4 * q + 2] + shift),
-                            v[4 * q + 3] * (base[4 * q + 3] + shift));
+                            v[4 * q] * (a[4 * q] + shift), v[4 * q + 1] * (a[4 * q + 1] + shift),
+                            v[4 * q + 2] * (a[4 * q + 2] + shift),
+                            v[4 * q + 3] * (a[4 * q + 3] + shift));
                 }
             } else {
 #pragma unroll
                 for (int q = 0; q < 4 * NV; ++q) {
                     const int e = l + G * q;
-                    if (e < E) out[e] = v[q] * (base[q] + shift);
+                    if (e < E) out[e] = v[q] * (a[q] + shift);
                 }
-            }
-        }
-        if (grad_w) {
-            // The k experts' elements again, with their dw'; an expert named twice gets the sum
-            // of its pairs' dw' (in pair order) from either lane.
-            const unsigned same = __match_any_sync(kFull, id >= 0 ? id : -1 - lane) & gmask;
-            __syncwarp();
-            float sum = dw;
-            if (__any_sync(kFull, id >= 0 && (same & (same - 1)))) {
-                sum = 0.0f;
-                for (int j = 0; j < G; ++j) {
-                    const float o = __shfl_sync(kFull, dw, (lane & ~(G - 1)) + j);
-                    if ((same >> ((lane & ~(G - 1)) + j)) & 1u) sum += o;
-                }
-            }
-            if (id >= 0) {
-                const float b = grad_losses ? scale * (float)counts[id] : 0.0f;
-                dlogits[t * E + id] = pj * (b + sum + shift);
             }
         }
     }
@@ -409,13 +464,13 @@ Grid grid_of(int T, const Shape& s) {
     g.threads = s.NV >= 8 ? 256 : 512;
     const int groups = g.threads / s.G;
     const long long need = std::max<long long>(1, ((long long)T + groups - 1) / groups);
-    if (need <= 2 * kMaxCluster) {
+    if (need <= 2 * (int)kMaxCluster) {
         g.cluster = 1;
-        while (g.cluster < kMaxCluster && g.cluster < need) g.cluster *= 2;
+        while (g.cluster < (int)kMaxCluster && g.cluster < need) g.cluster *= 2;
         g.blocks = g.cluster;
     } else {
         g.cluster = kMaxCluster;
-        const long long clusters = std::min<long long>((need + kMaxCluster - 1) / kMaxCluster,
+        const long long clusters = std::min<long long>((need + kMaxCluster - 1) / (int)kMaxCluster,
                                                        kMaxClusters);
         g.blocks = (int)clusters * kMaxCluster;
     }
@@ -460,7 +515,9 @@ void run_backward(const float* logits, const int32_t* ids, const uint8_t* mask,
     constexpr int threads = kThreadsOf<NV>;
     const long long need = ((long long)T + threads / G - 1) / (threads / G);
     const int blocks = (int)std::min<long long>(need, 148LL * 4);
-    launch_pdl(route_backward_kernel<G, NV, VEC>, dim3(blocks), dim3(threads), 0, s, logits, ids,
+    // Rows of dw' (float) and of their lanes (byte): at most 16 x 512 x 5 bytes, below 48 KB.
+    const size_t smem = grad_w ? (size_t)(threads / G) * E * 5 : 0;
+    launch_pdl(route_backward_kernel<G, NV, VEC>, dim3(blocks), dim3(threads), smem, s, logits, ids,
                mask, counts, grad_losses, grad_w, T, E, k, renorm, dlogits, st);
 }
 
@@ -495,7 +552,8 @@ void launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask
     }
     *launches += 1;
     if (g.blocks > g.cluster) {
-        launch_pdl(balance_final_kernel, dim3(1), dim3(1024), 0, s, (const float*)part,
+        const size_t smem = (size_t)std::max(1024, 2 * (E + 1)) * 4;
+        launch_pdl(balance_final_kernel, dim3(1), dim3(1024), smem, s, (const float*)part,
                    g.blocks / g.cluster, E, k, losses, counts, probs);
         *launches += 1;
     }
