@@ -1,6 +1,7 @@
 // common.cuh -- device helpers shared by the MoE kernels (sm_100a only).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -229,6 +230,20 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.attrs = at;
     cfg.numAttrs = 1;
     return note_launch(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device (raised as needed; a
+// kernel's limit is asked for once per device, as the driver call costs a microsecond).
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), std::atomic<int> (&allowed)[64], int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return note_launch(e);
+    if (dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = note_launch(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         bytes));
+    if (e == cudaSuccess && dev < 64) allowed[dev].store(bytes, std::memory_order_relaxed);
+    return e;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

@@ -204,8 +204,10 @@ int w4_rows1(const moe_problem* p) {          // rows of W1 per expert
 }
 
 // Rows per expert (the batch's largest average) up to which the products read the 4-bit weights
-// directly; above it the weights are first read back to bfloat16 for the tensor-core GEMM.
-constexpr long long kW4DirectRows = 96;
+// directly; above it the weights are first read back to bfloat16 for the tensor-core GEMM.  (64
+// experts of 2048 x 1024, both products, direct and read back: 16 rows 84 and 216 us, 48 rows 173 and
+// 219, 64 rows 228 and 238, 96 rows 327 and 226.)
+constexpr long long kW4DirectRows = 64;
 
 bool w4_direct(const moe_problem* p) {
     return max_rows_of(p, capacity_of(p)) <= kW4DirectRows * p->E;

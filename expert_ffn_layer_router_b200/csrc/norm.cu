@@ -561,11 +561,9 @@ bool wide_ok(int d, int elem_bytes, std::initializer_list<const void*> ptrs) {
 }
 
 template <class Kern, class... Args>
-void launch_norm(Kern kern, int blocks, int wpr, int smem, cudaStream_t s, Args... args) {
-    if (smem > 48 * 1024 &&
-        note_launch(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem)) != cudaSuccess)
-        return;
+void launch_norm(Kern kern, std::atomic<int> (&allowed)[64], int blocks, int wpr, int smem,
+                 cudaStream_t s, Args... args) {
+    if (smem > 48 * 1024 && allow_smem(kern, allowed, smem) != cudaSuccess) return;
     launch_pdl(kern, dim3(blocks), dim3((wpr > 8 ? wpr : 8) * 32), smem, s, args...);
 }
 
@@ -574,7 +572,8 @@ void forward_typed(const T* x, const float* gamma, const float* beta, float eps,
                    T* y, float* mean, float* rstd, cudaStream_t s) {
     auto go = [&](auto kern, auto wpr) {
         constexpr int W = decltype(wpr)::value;
-        launch_norm(kern, norm_blocks(rows, d, 3), W, Ring<T, VB, 1, kWarpsOf<W> * 32>::kBytes, s,
+        static std::atomic<int> allowed[64];      // (one for each instance of this lambda)
+        launch_norm(kern, allowed, norm_blocks(rows, d, 3), W, Ring<T, VB, 1, kWarpsOf<W> * 32>::kBytes, s,
                     x, gamma, beta, eps, rows, d, y, mean, rstd);
     };
     switch (warps_per_row(d)) {
@@ -604,7 +603,8 @@ void backward_typed(const T* dy, const T* x, const float* gamma, const float* me
                     cudaStream_t s) {
     auto go = [&](auto kern, auto wpr) {
         constexpr int W = decltype(wpr)::value;
-        launch_norm(kern, backward_blocks(rows, d), W, Ring<T, VB, 3, kWarpsOf<W> * 32>::kBytes, s,
+        static std::atomic<int> allowed[64];      // (one for each instance of this lambda)
+        launch_norm(kern, allowed, backward_blocks(rows, d), W, Ring<T, VB, 3, kWarpsOf<W> * 32>::kBytes, s,
                     dy, x, gamma, mean, rstd, dres, rows, d, dx, part);
     };
     switch (warps_per_row(d)) {

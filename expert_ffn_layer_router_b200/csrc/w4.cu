@@ -270,9 +270,9 @@ __global__ void __launch_bounds__(256)
 // The grouped products: D[r, n] = act(sum_k W[e]_nk A[row(r), k] + bias[e][n]) for the rows r of
 // each expert e.
 //
-// A unit is (expert, 32 UG features, up to 32 / KS rows); one persistent block per SM, of 16 product
-// warps and two copying warps, takes an equal run of the list of units.  A step of a unit is KS
-// chunks of 128 columns (KS = 2, 4 or 8, UG = 16 / KS): warp w works on 32 features (w / KS) and on
+// A unit is (expert, 32 UG features, up to 32 / KS rows); persistent blocks (two per SM) of 8 product
+// warps and two copying warps take equal runs of the list of units.  A step of a unit is KS chunks
+// of 128 columns (KS = 2, 4 or 8, UG = 8 / KS): warp w works on 32 features (w / KS) and on
 // chunk w % KS of the step; the KS sums are added through shared memory in a fixed order at the
 // unit's end.  Many units: KS = 2; few (one token): KS = 8 spreads K over the warps.
 //
@@ -307,21 +307,22 @@ struct W4Args {
     DeviceStatus* st;
 };
 
-constexpr int kWarps = 16;                         // product warps
+constexpr int kWarps = 8;                          // product warps
 constexpr int kThreads = (kWarps + 2) * 32;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kLines = 16;                         // row pieces of a stage (rows x boxes)
 constexpr int kLineBytes = 512 + 64;               // 256 columns, padded: neighbours differ in bank
 constexpr int kStageX = kLines * kLineBytes;
-constexpr int kStageW = 256 * 128;                 // 32 UG features x KS chunks of 128 columns
+constexpr int kStageW = 128 * 128;                 // 32 UG features x KS chunks of 128 columns
 constexpr int kRedStride = 36;                     // floats per row of the partial sums
 constexpr int kRedBytes = kWarps * 8 * kRedStride * 4;
 
 // A stage: weights (128-byte rows, 16-byte pieces swizzled by the row), rows, scales (and offsets).
 template <int G>
-constexpr int kSideBytes = 512 * (256 / G);
+constexpr int kSideBytes = 256 * (256 / G);
 template <bool ZERO, int G>
-constexpr int kStageBytes = kStageW + kStageX + (ZERO ? 2 : 1) * kSideBytes<G>;
+constexpr int kStageBytes =
+    kStageW + kStageX + ((ZERO ? 2 : 1) * kSideBytes<G> + 1023) / 1024 * 1024;
 // (1024 bytes to align the ring; row pointers of the unit being copied; 2 flags)
 template <bool ZERO, int G>
 constexpr int w4_smem_bytes(int E) {
@@ -344,6 +345,7 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
+
 // 16 bytes to shared memory: copied (bytes = 16) or zeros (bytes = 0).
 __device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -361,7 +363,7 @@ struct W4Kernel {
     const W4Args& a;
     const int* s_pre;         // units before each expert
     int S, groups, nfb;       // 256-column boxes of K, groups of K, feature blocks
-    int UG, row_tile;         // 16 >> lks, 32 >> lks
+    int UG, row_tile;         // 8 >> lks, 32 >> lks
 
     __device__ __forceinline__ Unit unit_at(int u) const {
         int lo = 0, hi = a.E - 1;                 // largest e with s_pre[e] <= u
@@ -481,7 +483,7 @@ struct W4Kernel {
 };
 
 template <int EPI, bool ZERO, int G>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tm, const W4Args args) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr int kStage = kStageBytes<ZERO, G>;
@@ -499,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.S = (args.K + 255) / 256;
     w.groups = (args.K + G - 1) / G;
     w.UG = kWarps >> args.lks;
-    w.nfb = (args.N / 32 + w.UG - 1) >> (4 - args.lks);
+    w.nfb = (args.N / 32 + w.UG - 1) >> (3 - args.lks);
     w.row_tile = 2 * kLines >> args.lks;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = args.E;
@@ -622,11 +624,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 there |= (src != nullptr ? 1u : 0u) << i;
                 line[i] = src ? src + lane * 8 : args.A;
             }
-            // Scales: piece i of the lane belongs to group i NB + lg of the step; 8 features from
+            // Scales: piece i of the lane belongs to group i KS + lg of the step; 8 features from
             // f (past the end: none).
-            const int lg = lane >> (6 - args.lks), piece = lane & (4 * w.UG - 1);
+            const int lg = lane >> (5 - args.lks), piece = lane & (4 * w.UG - 1);
             const int f = w.first(x, piece >= 2 * w.UG) + (piece & (2 * w.UG - 1)) * 8;
-            const long long per_step = (long long)NB * args.N;
+            const long long per_step = (long long)KS * args.N;
             long long side = ((long long)x.e * w.groups + lg) * args.N + f;
             int left = f < args.N ? w.groups - lg : 0;       // groups from this lane's first on
             int cols = args.K - lane * 8;                    // columns from this lane's piece on
@@ -642,14 +644,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (cols > NB * 256) line[i] += NB * 256;    // (stays inside the row)
                 }
 #pragma unroll
-                for (int i = 0; i < W4Kernel<EPI, ZERO, G>::kPer; ++i) {
+                for (int i = 0; i < W4Kernel<EPI, ZERO, G>::kPer / 2; ++i) {
                     const bool in = left > 0;
                     const uint32_t d = dst + kStageX + 32 * i * 16;
                     cp_async_16z(d, args.scale + (in ? side : 0), in ? 16 : 0);
                     if constexpr (ZERO)
                         cp_async_16z(d + kSideBytes<G>, args.zero + (in ? side : 0), in ? 16 : 0);
                     side += per_step;
-                    left -= NB;
+                    left -= KS;
                 }
                 cp_async_arrive_noinc(full_bar(slot));
                 if (++slot == kStages) {
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mine[8 * q] = acc[n][q >> 1][i + 2 * (q & 1)];
             }
-            asm volatile("bar.sync 1, 512;" ::: "memory");
+            asm volatile("bar.sync 1, 256;" ::: "memory");
             // Thread i < 64 UG joins 4 features of a row: (group, row, g).
             const int i = threadIdx.x, jg = i >> 6, row = (i >> 3) & 7, fg = i & 7;
             const int jb = x.fb * w.UG + jg;
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int r = 0; r < 4; ++r) v[r] += s[q * 8 * kRedStride + 8 * r];
                 w.store(x, jb, fg, n * 8 + row, v);
             }
-            asm volatile("bar.sync 1, 512;" ::: "memory");
+            asm volatile("bar.sync 1, 256;" ::: "memory");
         }
     }
 }
@@ -736,9 +738,10 @@ template <int EPI, bool ZERO, int G>
 cudaError_t run_w4(const CUtensorMap& tm, const W4Args& a, cudaStream_t s) {
     auto kern = w4_gemm_kernel<EPI, ZERO, G>;
     const int smem = w4_smem_bytes<ZERO, G>(a.E);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (note_launch(e) != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(kSm), dim3(kThreads), smem, s, tm, a);
+    static std::atomic<int> allowed[64];
+    const cudaError_t e = allow_smem(kern, allowed, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(2 * kSm), dim3(kThreads), smem, s, tm, a);
 }
 
 template <int EPI>
@@ -827,10 +830,9 @@ cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int 
                            int* launches) {
     W4Args a{(const uint16_t*)A, a_rows, a_row_limit, offsets, E, K, N, max_rows, scale, zero,
              bias, (uint16_t*)D, ldd, 1, st};
-    // Warps that share a unit's K: the fewest that give every block a unit, at most 8 and no more
-    // than there are chunks.  (One token, 8 experts of 2048 x 1024: 26, 22 and 20 us for KS = 2, 4
-    // and 8, and 27 for 16, whose rows fill 2 of the 8 columns of an instruction; 64 tokens, all
-    // experts: 74, 86 and 166 us.)
+    // Warps that share a unit's K: the fewest that give every SM a unit, at most 8 and no more than
+    // there are chunks.  (Both products, 64 experts of 2048 x 1024, KS = 2, 4, 8: 1 token 22, 17,
+    // 16 us; 2 tokens 23, 20, 23; 4 tokens 29, 30, 33; 64 tokens 64, 77, 152.)
     while (a.lks < 3 && (256 << a.lks) <= K &&
            (long long)std::min(E, max_rows) * (N / 32) < (long long)kSm * (kWarps >> a.lks))
         a.lks += 1;

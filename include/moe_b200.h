@@ -256,7 +256,7 @@ moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes);
  * MOE_FLAG_GATED), W2 [E, d_model, d_ff]; their groups may differ.  p's dtype is MOE_BF16 (else
  * MOE_ERR_UNSUPPORTED), with moe_expert_ffn's rules for widths, alignment, offsets and rowtok; rows
  * of Y behind offsets[E] are left as they were.
- * Few rows per expert (min(T k, E K) <= 96 E): the products read the 4-bit weights and form
+ * Few rows per expert (min(T k, E K) <= 64 E): the products read the 4-bit weights and form
  * sum_k (nibble - 8) x_k per group exactly in float32 before the scale; b1, b2 nullable.  More rows:
  * each weight is first read back to bfloat16 (one rounding per value) into the workspace, for the
  * grouped tensor-core GEMM.  The hidden activations are kept in bfloat16 either way. */

@@ -569,8 +569,8 @@ FFN = [  # T, d, F, E, k, groups, zeros, gated, kind
     (65, 1472, 128, 9, 3, (128, 128), True, False, "random"),
     (100, 1024, 512, 300, 2, (32, 64), False, False, "random"),
     (129, 512, 1408, 8, 3, (128, 32), True, True, "random"),
-    (96, 256, 256, 1, 1, (64, 64), True, False, "hot"),
-    (97, 256, 256, 1, 1, (64, 64), True, False, "hot"),      # above the rows the direct path takes
+    (64, 256, 256, 1, 1, (64, 64), True, False, "hot"),
+    (65, 256, 256, 1, 1, (64, 64), True, False, "hot"),      # above the rows the direct path takes
     (700, 512, 384, 6, 2, (32, 128), False, True, "random"),
     (1100, 320, 192, 4, 2, (64, 64), True, False, "hot"),
 ]
@@ -585,7 +585,7 @@ def test_expert_ffn_w4(moe, T, d, F, E, k, groups, zeros, gated, kind):
     x = randn(g, T, d).to(torch.bfloat16)
     offsets, rowtok = routing(g, T, E, k, kind)
     layer = moe.MoELayer(T, d, F, E, k, flags=moe.FLAG_GATED if gated else 0, w4=True)
-    copy = T * k > 96 * E
+    copy = T * k > 64 * E
     for bias in (True, False):
         bb = (b1, b2) if bias else (None, None)
         Y = layer.expert_ffn_w4(x, offsets, rowtok, W1, bb[0], W2, bb[1])
@@ -705,7 +705,7 @@ def test_block_with_norm_and_w4(moe, T, E, k, C):
     r = layer.route(logits)
     for key in ("ids", "w", "slot", "drop", "counts"):
         assert torch.equal(rt[key + "_out"], r[key]), key
-    copy = layer.max_rows > 96 * E
+    copy = layer.max_rows > 64 * E
     ref, tol = block_reference(
         i["x"], y, rt, lambda rows, off, tok: ffn_reference(rows, off, tok, W1, i["b1"], W2,
                                                             i["b2"], False, copy), d)

@@ -147,14 +147,14 @@ def test_block_refusals(moe):
 
 def test_workspace_sizes(moe):
     """The 4-bit workspace holds one bfloat16 copy of the larger weight exactly when an expert's
-    average share passes 96 rows."""
-    for T, d, F, E, k, flags in ((64, 2048, 1024, 64, 8, 0), (96, 64, 64, 2, 2, 0),
-                                 (97, 64, 64, 2, 2, 0), (4096, 2048, 1408, 64, 6, 0),
+    average share passes 64 rows."""
+    for T, d, F, E, k, flags in ((64, 2048, 1024, 64, 8, 0), (64, 64, 64, 2, 2, 0),
+                                 (65, 64, 64, 2, 2, 0), (4096, 2048, 1408, 64, 6, 0),
                                  (500, 256, 128, 4, 2, 4)):
         p = moe.problem(T, d, F, E, k, math.inf, "bf16", flags)
         plain, packed = moe.moe_workspace_size(p), moe.moe_workspace_size_packed(p)
         copy = E * d * max(F * (2 if flags else 1), F) * 2
-        assert packed - plain == (0 if T * k <= 96 * E else -(-copy // 256) * 256)
+        assert packed - plain == (0 if T * k <= 64 * E else -(-copy // 256) * 256)
     n = ctypes.c_size_t()
     L = moe.lib()
     assert L.moe_workspace_size_packed(prob(moe, dtype=0), ctypes.byref(n)) == 2
