@@ -74,6 +74,10 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     }
 }
 
+// exp(x), x <= 0, through the hardware's 2^t: the product x log2(e) is off by |x| 2^-24 relative to the
+// result, like the rounding of x = L - max itself, and 2^t by 2 ulp.
+__device__ __forceinline__ float exp_of(float x) { return __expf(x); }
+
 // v := exp(v - max); returns (max, sum).  A row that is not live gives max = 0, sum = 1 and zeros.
 template <int G, int NV>
 __device__ __forceinline__ float2 softmax_terms(float (&v)[4 * NV], bool live) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ float2 softmax_terms(float (&v)[4 * NV], bool live) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4 * NV; ++i) {
-        v[i] = expf(v[i] - m);
+        v[i] = exp_of(v[i] - m);
         s += v[i];
     }
     s = group_sum<G>(s);
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kThreadsOf<NV>, 2)
         coming = t < t1 && (!mask || mask[t]);
         load_row<G, NV, VEC>(logits + (long long)t * E, E, l, coming, next);
         const float2 ms = softmax_terms<G, NV>(v, live);
-        const float r = 1.0f / ms.y;
+        const float r = __frcp_rn(ms.y);
 #pragma unroll
         for (int q = 0; q < 4 * NV; ++q) acc[q] = fmaf(v[q], r, acc[q]);
         if (live && l == 0) {
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
         t += all;
         fetch();
         const float2 ms = softmax_terms<G, NV>(v, live);
-        const float r = 1.0f / ms.y;
+        const float r = __frcp_rn(ms.y);
         float a[4 * NV];
 #pragma unroll
         for (int q = 0; q < 4 * NV; ++q) a[q] = base[q];
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
                 dw = 0.0f;
             }
             if (renorm) {
-                const float pj = id >= 0 ? expf(logits[at * E + id] - ms.x) * r : 0.0f;
+                const float pj = id >= 0 ? exp_of(logits[at * E + id] - ms.x) * r : 0.0f;
                 const float S = group_sum<G>(pj);
                 const float d = group_sum<G>(dw * pj);
                 dw = S > 0.0f ? (dw - d / S) / S : 0.0f;
