@@ -170,17 +170,17 @@ __global__ void __launch_bounds__(kThreadsOf<NV>, 2)
     __shared__ float s_buf[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int l = lane & (G - 1);
-    const int t0 = min((long long)T, (long long)blockIdx.x * rows_per_block);
-    const int t1 = min((long long)T, (long long)t0 + rows_per_block);
+    const long long t0 = min((long long)T, (long long)blockIdx.x * rows_per_block);
+    const long long t1 = min((long long)T, t0 + rows_per_block);
 
     for (int e = threadIdx.x; e < E; e += kThreads) s_cnt[e] = 0;
     __syncthreads();
     // Pair counts of the block's tokens.
-    for (int t = t0 + threadIdx.x; t < t1; t += kThreads) {
+    for (long long t = t0 + threadIdx.x; t < t1; t += kThreads) {
         if (mask && !mask[t]) continue;
 #pragma unroll 8
         for (int j = 0; j < k; ++j) {
-            const int e = ids[(long long)t * k + j];
+            const int e = ids[t * k + j];
             if (e >= 0 && e < E) atomicAdd(&s_cnt[e], 1);
             else report(st, MOE_DEV_BAD_INDEX, 610);
         }
@@ -192,11 +192,11 @@ __global__ void __launch_bounds__(kThreadsOf<NV>, 2)
     float n = 0.0f;
     // Every group of a warp makes the same number of steps (the shuffles name the whole warp).
     // The next row's logits are loaded before this one's sums.
-    const int steps = (t1 - t0 + kGroups - 1) / kGroups;
-    int t = t0 + threadIdx.x / G;
+    const int steps = (int)((t1 - t0 + kGroups - 1) / kGroups);
+    long long t = t0 + threadIdx.x / G;
     bool coming = t < t1 && (!mask || mask[t]);
     float next[4 * NV];
-    load_row<G, NV, VEC>(logits + (long long)t * E, E, l, coming, next);
+    load_row<G, NV, VEC>(logits + t * E, E, l, coming, next);
     for (int i = 0; i < steps; ++i) {
         const bool live = coming;
         float v[4 * NV];
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreadsOf<NV>, 2)
         for (int q = 0; q < 4 * NV; ++q) v[q] = next[q];
         t += kGroups;
         coming = t < t1 && (!mask || mask[t]);
-        load_row<G, NV, VEC>(logits + (long long)t * E, E, l, coming, next);
+        load_row<G, NV, VEC>(logits + t * E, E, l, coming, next);
         const float2 ms = softmax_terms<G, NV>(v, live);
         const float r = __frcp_rn(ms.y);
 #pragma unroll

@@ -191,12 +191,20 @@ moe_status ffn_steps(const moe_problem* p, const void* x, const int32_t* offsets
     return MOE_OK;
 }
 
+constexpr int32_t kNormMaxCols = 1 << 30;       // columns are counted in 32 bits
+
 // ---- 4-bit weights ----
 bool bad_group(int32_t g) { return g != 32 && g != 64 && g != 128; }
 
 bool bad_w4(const moe_w4* w) {
     return !w || !w->q || !w->scale || bad_group(w->group) || misaligned(w->q, 16) ||
            misaligned(w->scale, 16) || misaligned(w->zero, 16);
+}
+
+// Rows of a 4-bit weight are addressed by 32-bit numbers in the copies' tensor maps.
+bool w4_too_many_rows(const moe_problem* p) {
+    const long long n1 = (p->flags & MOE_FLAG_GATED) ? 2LL * p->d_ff : p->d_ff;
+    return (long long)p->E * std::max<long long>(n1, p->d_model) > 0x7fffffffLL;
 }
 
 int w4_rows1(const moe_problem* p) {          // rows of W1 per expert
@@ -646,7 +654,8 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
 
 moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes) {
     if (bad_problem(p) || !bytes) return MOE_ERR_INVALID_ARG;
-    if (p->dtype != MOE_BF16 || unsupported(p)) return MOE_ERR_UNSUPPORTED;
+    if (p->dtype != MOE_BF16 || unsupported(p) || w4_too_many_rows(p))
+        return MOE_ERR_UNSUPPORTED;
     *bytes = make_plan(p).total + w4_copy_bytes(p);
     return MOE_OK;
 }
@@ -687,7 +696,7 @@ moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int3
                              size_t ws_bytes, void* stream) {
     moe_status r = pre(p, true);
     if (r != MOE_OK) return r;
-    if (p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (p->dtype != MOE_BF16 || w4_too_many_rows(p)) return MOE_ERR_UNSUPPORTED;
     if (!offsets || bad_w4(W1) || bad_w4(W2) || (p->T > 0 && (!x || !rowtok || !Y)))
         return MOE_ERR_INVALID_ARG;
     if (misaligned(x, 16) || misaligned(Y, 16) || misaligned(b1, 16) || misaligned(b2, 16))
@@ -711,6 +720,7 @@ moe_status moe_layer_norm(const moe_problem* p, const void* x, const float* gamm
         (p->T > 0 && (!x || !y || !mean || !rstd)))
         return MOE_ERR_INVALID_ARG;
     if (y && y == x) return MOE_ERR_INVALID_ARG;
+    if (p->d_model > kNormMaxCols) return MOE_ERR_UNSUPPORTED;
     int launches = 0;
     if (p->T > 0)
         moe::launch_layer_norm(p->dtype, x, gamma, beta, eps, p->T, p->d_model, y, mean, rstd,
@@ -727,6 +737,7 @@ moe_status moe_layer_norm_backward(const moe_problem* p, const void* dy, const v
     if (!gamma || !dgamma || !dbeta || (p->T > 0 && (!dy || !x || !mean || !rstd || !dx)))
         return MOE_ERR_INVALID_ARG;
     if (dx && (dx == x || dx == dy || dx == dres)) return MOE_ERR_INVALID_ARG;
+    if (p->d_model > kNormMaxCols) return MOE_ERR_UNSUPPORTED;
     Plan q;
     if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
     cudaStream_t s = (cudaStream_t)stream;
@@ -792,7 +803,8 @@ moe_status moe_forward_block(const moe_problem* p, const void* x, const moe_norm
     moe_status r = pre(p, true);
     if (r != MOE_OK) return r;
     const bool w4 = Q1 || Q2;
-    if (w4 && p->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (w4 && (p->dtype != MOE_BF16 || w4_too_many_rows(p))) return MOE_ERR_UNSUPPORTED;
+    if (norm && p->d_model > kNormMaxCols) return MOE_ERR_UNSUPPORTED;
     if (!Wr || (p->T > 0 && (!x || !out)) || (out && out == x)) return MOE_ERR_INVALID_ARG;
     if (w4 ? (W1 || W2 || bad_w4(Q1) || bad_w4(Q2)) : (!W1 || !W2)) return MOE_ERR_INVALID_ARG;
     if (norm) {

@@ -372,16 +372,19 @@ class W4Weights:
     moe_w4).  :func:`quantize_w4` makes them."""
 
     def __init__(self, q, scale, zero=None, *, K, group):
-        self.q, self.scale, self.zero = q, scale, zero
-        self.E, self.N, self.K, self.group = q.shape[0], q.shape[1], int(K), int(group)
-        if self.group not in (32, 64, 128):
+        E, N = q.shape[:2]
+        if group not in (32, 64, 128):
             raise MoeError(MOE_ERR_INVALID_ARG, "W4Weights: group must be 32, 64 or 128")
-        dev = q.device
-        _need("W4Weights", "q", q, torch.int32, (self.E, self.N, 16 * (-(-self.K // 128))), dev)
-        side = (self.E, -(-self.K // self.group), self.N)
+        dev, side = q.device, (E, -(-K // group), N)
+        _need("W4Weights", "q", q, torch.int32, (E, N, 16 * (-(-K // 128))), dev)
         _need("W4Weights", "scale", scale, torch.bfloat16, side, dev)
         if zero is not None:
             _need("W4Weights", "zero", zero, torch.bfloat16, side, dev)
+        self._set(q, scale, zero, E, N, K, group)
+
+    def _set(self, q, scale, zero, E, N, K, group):
+        self.q, self.scale, self.zero = q, scale, zero
+        self.E, self.N, self.K, self.group = E, N, int(K), int(group)
         self.c = W4(q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
                     self.group)
 
@@ -407,7 +410,9 @@ def quantize_w4(W, group, zeros=False, stream=None) -> W4Weights:
         scale = torch.empty(side, dtype=torch.bfloat16, device=W.device)
         zero = torch.empty(side, dtype=torch.bfloat16, device=W.device) if zeros else None
         moe_quantize_packed(W, E, N, K, group, q, scale, zero, st)
-    return W4Weights(q, scale, zero, K=K, group=group)
+    w = W4Weights.__new__(W4Weights)
+    w._set(q, scale, zero, E, N, K, group)
+    return w
 
 
 def dequantize_w4(w: W4Weights, stream=None):

@@ -497,6 +497,33 @@ def test_quantize_leaves_what_is_behind(moe):
     assert (out[E * N * K:] == -7).all()
 
 
+def test_offsets_past_32_bits(moe):
+    """More than 2^31 elements: the last rows and experts come out like small tensors do."""
+    g = gen(77)
+    E, N, K = 9, 65536, 4096
+    W = torch.zeros(E, N, K, dtype=torch.bfloat16, device=dev())
+    last = (randn(g, 1, 64, K) / 64).to(torch.bfloat16)
+    W[-1, -64:] = last[0]
+    w, small = moe.quantize_w4(W, 128), moe.quantize_w4(last, 128)
+    assert torch.equal(w.q[-1, -64:], small.q[0])
+    assert torch.equal(w.scale[-1, :, -64:], small.scale[0])
+    del W
+    back = moe.dequantize_w4(w)
+    assert torch.equal(back[-1, -64:], moe.dequantize_w4(small)[0])
+    assert (back[0, :64] == 0).all()
+    del back, w
+    T, d = 270000, 8192
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=dev())
+    x[-8:] = randn(g, 8, d).to(torch.bfloat16)
+    ga, be = randn(g, d), randn(g, d)
+    layer, few = moe.MoELayer(T, d, 64, 1, 1), moe.MoELayer(8, d, 64, 1, 1)
+    y, mean, rstd = layer.layer_norm(x, ga, be)
+    ys, ms, rs = few.layer_norm(x[-8:].contiguous(), ga, be)
+    assert torch.equal(y[-8:], ys) and torch.equal(mean[-8:], ms) and torch.equal(rstd[-8:], rs)
+    dx = layer.layer_norm_backward(y, x, ga, mean, rstd)[0]
+    assert torch.equal(dx[-8:], few.layer_norm_backward(ys, x[-8:].contiguous(), ga, ms, rs)[0])
+
+
 # ----------------------------------------------------------------------------------------------
 # Expert FFN over 4-bit weights
 # ----------------------------------------------------------------------------------------------
@@ -814,6 +841,41 @@ def test_streams_and_graphs(moe, T):
         graph.replay()
         torch.cuda.synchronize()
         for a, b in zip(all_operators(*args), kept):
+            assert torch.equal(a, b)
+
+
+def test_two_graphs_share_a_workspace(moe):
+    """Graphs captured over one workspace and replayed in turn, with plain calls between them, do not
+    disturb each other."""
+    T, d, F, E, k = 3000, 128, 128, 16, 2
+    g = gen(43)
+    layer = moe.MoELayer(T, d, F, E, k, w4=True)
+    W1, W2 = make_experts(moe, g, E, F, F, d, (64, 64), False)
+    logits = [randn(g, T, E) for _ in range(2)]
+    ids = [torch.topk(x, k, dim=1).indices.to(torch.int32) for x in logits]
+    x = [randn(g, T, d).to(torch.bfloat16) for _ in range(2)]
+    ga = 1 + 0.1 * randn(g, d)
+    route = [routing(g, T, E, k, "random") for _ in range(2)]
+
+    def work(i):
+        y, mean, rstd = layer.layer_norm(x[i], ga, ga)
+        return (*layer.balance_loss(logits[i], ids[i]),
+                *layer.layer_norm_backward(y, x[i], ga, mean, rstd),
+                layer.expert_ffn_w4(y, *route[i], W1, None, W2, None))
+
+    want = [work(0), work(1)]
+    graphs, kept = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            kept.append(work(i))
+    for i in (0, 1, 1, 0):
+        for t in kept[i]:
+            t.zero_()
+        graphs[i].replay()
+        for a, b in zip(work(1 - i), want[1 - i]):
+            assert torch.equal(a, b)
+        for a, b in zip(kept[i], want[i]):
             assert torch.equal(a, b)
 
 

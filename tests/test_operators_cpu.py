@@ -54,6 +54,10 @@ def test_layer_norm_refusals(moe):
     for eps in (-1e-9, math.nan, math.inf):
         assert L.moe_layer_norm(p, FAKE, FAKE, FAKE, eps, FAKE2, FAKE, FAKE, None) == 1
     assert L.moe_layer_norm(p, FAKE, FAKE, FAKE, 1e-5, FAKE, FAKE, FAKE, None) == 1     # y = x
+    wide = prob(moe, d=(1 << 30) + 1)
+    assert L.moe_layer_norm(wide, FAKE, FAKE, FAKE, 1e-5, FAKE2, FAKE, FAKE, None) == 2
+    assert L.moe_layer_norm_backward(wide, *[FAKE] * 5, None, FAKE2, FAKE, FAKE, FAKE, BIG,
+                                     None) == 2
     good = [FAKE] * 5 + [None, FAKE2, FAKE, FAKE]
     for i in (0, 1, 2, 3, 4, 6, 7, 8):
         a = list(good)
@@ -110,6 +114,8 @@ def test_packed_weight_refusals(moe):
     ffn = L.moe_expert_ffn_packed
     assert ffn(prob(moe, dtype=0), FAKE, FAKE, FAKE, ok, None, ok, None, FAKE, FAKE, BIG, None) == 2
     assert ffn(prob(moe, d=96), FAKE, FAKE, FAKE, ok, None, ok, None, FAKE, FAKE, BIG, None) == 2
+    assert ffn(prob(moe, E=1024, F=1 << 21), FAKE, FAKE, FAKE, ok, None, ok, None, FAKE, FAKE, BIG,
+               None) == 2
     assert ffn(prob(moe, flags=4), FAKE, FAKE, FAKE, ok, None, ok, None, FAKE, FAKE, BIG, None) == 2
     for i in (0, 1, 2, 7):
         a = [FAKE, FAKE, FAKE, ok, None, ok, None, FAKE]
