@@ -126,7 +126,8 @@ void launch_w4_quantize(int dtype, const void* W, int E, int N, int K, int G, ui
 void launch_w4_dequantize(const uint32_t* q, const uint16_t* scale, const uint16_t* zero, int E,
                           int N, int K, int G, void* W, cudaStream_t s, int* launches);
 // Grouped products over 4-bit weights [E, N, K] for few rows per expert.  which = 0: D = SiLU(A
-// W^T + bias), 1: D = A W^T + bias, 2: gated (N = 2 F rows of W, F columns of D).
+// W^T + bias), 1: D = A W^T + bias, 2: gated (N = 2 F rows of W, F columns of D).  a_rows = null:
+// the launch before this one on the stream is the first product, which wrote A.
 cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int a_row_limit,
                            const int32_t* offsets, int E, int K, int N, int max_rows,
                            const uint32_t* q, const uint16_t* scale, const uint16_t* zero, int G,

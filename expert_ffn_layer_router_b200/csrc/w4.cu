@@ -303,6 +303,7 @@ struct W4Args {
     const float* bias;        // [E, N], nullable
     uint16_t* D;
     int ldd;
+    bool early;               // the launch before this one wrote A alone: all else may start first
     int lks;                  // log2 of KS, the warps that share a unit's K (2, 4 or 8)
     DeviceStatus* st;
 };
@@ -513,7 +514,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&tm) : "memory");
     }
-    pdl_begin();
+    // Second product: offsets and weights were complete before the first one began (it waited for
+    // its predecessors), so the list of units is made and weights are copied while the first one's
+    // last blocks run; the warp that copies the rows waits for it.
+    if (!args.early) pdl_begin();
     if (warp == 0) {
         // Units before each expert; offsets are checked as the grouped GEMM does: 0 first,
         // non-decreasing, at most max_rows.  Bad offsets: nothing is computed or stored.
@@ -544,10 +548,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     __syncthreads();
-    if (*s_bad) return;
+    if (*s_bad) {
+        if (args.early) pdl_begin();
+        return;
+    }
     const int total = s_pre[E];
-    const int u0 = (int)((long long)total * blockIdx.x / gridDim.x);
-    const int u1 = (int)((long long)total * (blockIdx.x + 1) / gridDim.x);
+    // Equal runs of units.  Blocks i and i + 148 usually share an SM: they take neighbouring runs, so
+    // that an SM's two shares add up to within one unit of the others'.
+    const int run = (int)(blockIdx.x % kSm * 2 + blockIdx.x / kSm);
+    const int u0 = (int)((long long)total * run / gridDim.x);
+    const int u1 = (int)((long long)total * (run + 1) / gridDim.x);
 
     if (warp == kWarps) {
         // ---- copies the weights ----
@@ -589,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (warp == kWarps + 1) {
         // ---- copies scales and rows: lane l the 16-byte piece l of every line of rows ----
+        if (args.early) pdl_begin();
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -829,7 +840,7 @@ cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int 
                            const float* bias, void* D, int ldd, DeviceStatus* st, cudaStream_t s,
                            int* launches) {
     W4Args a{(const uint16_t*)A, a_rows, a_row_limit, offsets, E, K, N, max_rows, scale, zero,
-             bias, (uint16_t*)D, ldd, 1, st};
+             bias, (uint16_t*)D, ldd, a_rows == nullptr, 1, st};
     // Warps that share a unit's K: the fewest that give every SM a unit, at most 8 and no more than
     // there are chunks.  (Both products, 64 experts of 2048 x 1024, KS = 2, 4, 8: 1 token 22, 17,
     // 16 us; 2 tokens 23, 20, 23; 4 tokens 29, 30, 33; 64 tokens 64, 77, 152.)
