@@ -160,7 +160,6 @@ constexpr int kWarpsOf = WPR > 8 ? WPR : 8;
 template <class T, int VB, int STREAMS, int THREADS>
 struct Ring {
     static constexpr bool kOn = VB > 1;
-    static constexpr int NV = kElems / VB;
     static constexpr int kRows = 8 / sizeof(T);                       // 4 (bfloat16) or 2
     static constexpr int kRowBytes = STREAMS * THREADS * kElems * (int)sizeof(T);
     static constexpr int kBytes = kOn ? kRows * kRowBytes : 0;
@@ -169,7 +168,7 @@ struct Ring {
 
     __device__ __forceinline__ explicit Ring(uint8_t* smem) : base(smem + threadIdx.x * 16), put(0), get(0) {}
     __device__ __forceinline__ uint8_t* at(int slot, int stream, int v) const {
-        return base + slot * kRowBytes + (stream * NV + v) * THREADS * 16;
+        return base + slot * kRowBytes + (stream * (kElems / VB) + v) * THREADS * 16;
     }
     __device__ __forceinline__ void copy(int stream, int v, const T* src) const {
         if constexpr (kOn) cp_async_16(smem_u32(at(put, stream, v)), src);

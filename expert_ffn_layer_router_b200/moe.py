@@ -440,7 +440,12 @@ class MoELayer:
         nbytes = moe_workspace_size_packed(self.p) if w4 else moe_workspace_size(self.p)
         # int64 elements keep the base 256-byte aligned through the caching allocator.
         self.ws = torch.zeros((nbytes + 7) // 8, dtype=torch.int64, device=self.device)
+        self._p = ctypes.byref(self.p)
         self.max_rows = min(T * k, E * self.K)
+
+    @property
+    def _ws(self):
+        return self.ws.data_ptr(), self.ws.numel() * self.ws.element_size()
 
     @property
     def torch_dtype(self):
@@ -525,14 +530,17 @@ class MoELayer:
         int32 (pairs per expert, then tokens), ``probs`` [E] (mean router probability).
         ``mask`` [T] uint8 or bool: 0 leaves a token out."""
         p, dev, what = self.p, self.ws.device, "balance_loss"
-        _need(what, "logits", logits, torch.float32, (p.T, p.E), dev)
-        _need(what, "ids", ids, torch.int32, (p.T, p.k), dev)
-        mask = self._mask(what, mask)
+        T, E = p.T, p.E
+        _need(what, "logits", logits, torch.float32, (T, E), dev)
+        _need(what, "ids", ids, torch.int32, (T, p.k), dev)
+        mask = None if mask is None else self._mask(what, mask)
         with _on(dev, stream) as st:
             losses = torch.empty(2, dtype=torch.float32, device=dev)
-            counts = torch.empty(p.E + 1, dtype=torch.int32, device=dev)
-            probs = torch.empty(p.E, dtype=torch.float32, device=dev)
-            moe_balance_loss(p, logits, ids, losses, counts, probs, self.ws, mask, st)
+            counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+            probs = torch.empty(E, dtype=torch.float32, device=dev)
+            _check(_lib.moe_balance_loss(self._p, logits.data_ptr(), ids.data_ptr(), _at(mask),
+                                         losses.data_ptr(), counts.data_ptr(), probs.data_ptr(),
+                                         *self._ws, st), what)
         return losses, counts, probs
 
     def route_backward(self, logits, ids, counts=None, grad_losses=None, grad_w=None, mask=None,
@@ -540,62 +548,66 @@ class MoELayer:
         """dlogits [T, E] from the gradient of the losses (``grad_losses`` [2] on the device, with
         ``counts`` from :meth:`balance_loss`) and of the routing weights (``grad_w`` [T, k])."""
         p, dev, what = self.p, self.ws.device, "route_backward"
-        _need(what, "logits", logits, torch.float32, (p.T, p.E), dev)
-        _need(what, "ids", ids, torch.int32, (p.T, p.k), dev)
+        T, E = p.T, p.E
+        _need(what, "logits", logits, torch.float32, (T, E), dev)
+        _need(what, "ids", ids, torch.int32, (T, p.k), dev)
         if grad_losses is not None:
             _need(what, "grad_losses", grad_losses, torch.float32, (2,), dev)
-            _need(what, "counts", counts, torch.int32, (p.E + 1,), dev)
+            _need(what, "counts", counts, torch.int32, (E + 1,), dev)
         if grad_w is not None:
-            _need(what, "grad_w", grad_w, torch.float32, (p.T, p.k), dev)
-        mask = self._mask(what, mask)
+            _need(what, "grad_w", grad_w, torch.float32, (T, p.k), dev)
+        mask = None if mask is None else self._mask(what, mask)
         with _on(dev, stream) as st:
-            dlogits = torch.empty((p.T, p.E), dtype=torch.float32, device=dev)
-            moe_route_backward(p, logits, ids, counts, dlogits, self.ws, grad_losses, grad_w,
-                               mask, st)
+            dlogits = torch.empty_like(logits)
+            _check(_lib.moe_route_backward(self._p, logits.data_ptr(), ids.data_ptr(), _at(mask),
+                                           _at(counts), _at(grad_losses), _at(grad_w),
+                                           dlogits.data_ptr(), *self._ws, st), what)
         return dlogits
 
     def _mask(self, what, mask):
-        if mask is None:
-            return None
         if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
             mask = mask.view(torch.uint8)
         _need(what, "mask", mask, torch.uint8, (self.p.T,), self.ws.device)
         return mask
 
     # -- layer norm -----------------------------------------------------------------------------
-    def _need_norm(self, what, x, *params):
-        p, dev = self.p, self.ws.device
-        _need(what, "x", x, self.torch_dtype, (p.T, p.d_model), dev)
-        for name, t in params:
-            _need(what, name, t, torch.float32, (p.d_model,), dev)
-
     def layer_norm(self, x, gamma, beta, eps=1e-5, stream=None):
         """(y, mean, rstd) of the layer norm of x [T, d_model]; gamma, beta [d_model] float32."""
-        p, dev = self.p, self.ws.device
-        self._need_norm("layer_norm", x, ("gamma", gamma), ("beta", beta))
+        p, dev, what = self.p, self.ws.device, "layer_norm"
+        T, d = p.T, p.d_model
+        _need(what, "x", x, self.torch_dtype, (T, d), dev)
+        _need(what, "gamma", gamma, torch.float32, (d,), dev)
+        _need(what, "beta", beta, torch.float32, (d,), dev)
         with _on(dev, stream) as st:
             y = torch.empty_like(x)
-            mean = torch.empty(p.T, dtype=torch.float32, device=dev)
-            rstd = torch.empty(p.T, dtype=torch.float32, device=dev)
-            moe_layer_norm(p, x, gamma, beta, eps, y, mean, rstd, st)
+            mean = torch.empty(T, dtype=torch.float32, device=dev)
+            rstd = torch.empty_like(mean)
+            _check(_lib.moe_layer_norm(self._p, x.data_ptr(), gamma.data_ptr(), beta.data_ptr(),
+                                       eps, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), st),
+                   what)
         return y, mean, rstd
 
     def layer_norm_backward(self, dy, x, gamma, mean, rstd, dres=None, stream=None):
         """(dx, dgamma, dbeta) from dy and the forward's x, mean and rstd; ``dres`` [T, d_model]
         (the residual's gradient) is added to dx."""
         p, dev, what = self.p, self.ws.device, "layer_norm_backward"
-        self._need_norm(what, x, ("gamma", gamma))
-        for name, t in (("dy", dy), ("dres", dres)):
-            if name == "dy" or t is not None:
-                _need(what, name, t, self.torch_dtype, (p.T, p.d_model), dev)
-        _need(what, "mean", mean, torch.float32, (p.T,), dev)
-        _need(what, "rstd", rstd, torch.float32, (p.T,), dev)
+        T, d, dtype = p.T, p.d_model, self.torch_dtype
+        _need(what, "dy", dy, dtype, (T, d), dev)
+        _need(what, "x", x, dtype, (T, d), dev)
+        if dres is not None:
+            _need(what, "dres", dres, dtype, (T, d), dev)
+        _need(what, "gamma", gamma, torch.float32, (d,), dev)
+        _need(what, "mean", mean, torch.float32, (T,), dev)
+        _need(what, "rstd", rstd, torch.float32, (T,), dev)
         with _on(dev, stream) as st:
             dx = torch.empty_like(x)
-            dgamma = torch.empty(p.d_model, dtype=torch.float32, device=dev)
-            dbeta = torch.empty(p.d_model, dtype=torch.float32, device=dev)
-            moe_layer_norm_backward(p, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, self.ws, dres,
-                                    st)
+            dgamma = torch.empty_like(gamma)
+            dbeta = torch.empty_like(gamma)
+            _check(_lib.moe_layer_norm_backward(self._p, dy.data_ptr(), x.data_ptr(),
+                                                gamma.data_ptr(), mean.data_ptr(),
+                                                rstd.data_ptr(), _at(dres), dx.data_ptr(),
+                                                dgamma.data_ptr(), dbeta.data_ptr(), *self._ws,
+                                                st), what)
         return dx, dgamma, dbeta
 
     # -- 4-bit expert weights -------------------------------------------------------------------
@@ -624,7 +636,10 @@ class MoELayer:
         self._need_experts(what, W1, b1, W2, b2)
         with _on(dev, stream) as st:
             Y = torch.empty((max(self.max_rows, 1), p.d_model), dtype=x.dtype, device=dev)
-            moe_expert_ffn_packed(p, x, offsets, rowtok, W1.c, b1, W2.c, b2, Y, self.ws, st)
+            _check(_lib.moe_expert_ffn_packed(self._p, x.data_ptr(), offsets.data_ptr(),
+                                              rowtok.data_ptr(), ctypes.byref(W1.c), _at(b1),
+                                              ctypes.byref(W2.c), _at(b2), Y.data_ptr(),
+                                              *self._ws, st), what)
         return Y
 
     # -- the layer as a block of a model --------------------------------------------------------
@@ -642,7 +657,8 @@ class MoELayer:
             _need(what, "br", br, torch.float32, (p.E,), dev)
         self._need_experts(what, W1, b1, W2, b2)
         if norm is not None:
-            self._need_norm(what, x, ("gamma", norm[0]), ("beta", norm[1]))
+            for name, t in (("gamma", norm[0]), ("beta", norm[1])):
+                _need(what, name, t, torch.float32, (p.d_model,), dev)
         with _on(dev, stream) as st:
             def new(*shape, dtype=torch.float32):
                 return torch.empty(shape, dtype=dtype, device=dev)
