@@ -46,8 +46,8 @@ __device__ __forceinline__ uint16_t bf16_round(float v) {
 // reciprocal or the remainder leaves the normal range, a thread divides.  Adding 1.5 * 2^23 + 8
 // rounds t half to even and leaves q in the low bits; the eight words of bits are joined as
 // acc = 16 acc + bits modulo 2^32, and the constant's share is taken off at the end.
-// (64 x 1024 x 2048 from bfloat16, 0.34 GB moved: with a division near halves 143 us, half of the
-// warps meeting one.)
+// (64 x 1024 x 2048 from bfloat16, 0.34 GB moved: 96 us, 52 at the copy bandwidth; issue-bound.  With a
+// division near halves 143 us, half of the warps meeting one.)
 // ------------------------------------------------------------------------------------------------
 constexpr float kRound = 12582920.0f;                  // 1.5 * 2^23 + 8 (even: halves stay halves)
 constexpr uint32_t kRoundBits = 0x4b400008u - 8u;      // its bits, without the 8
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(256)
             const bool in = n0 + r < N && k < K;
             float v[8];
             unpack8<T>(raw[i], v);
-            // (a group that lies past K or N gives scale 0 and is not stored; the columns of a group
-            // are all in or all out up to 64, and zeros past K inside a group of 128 change only the
-            // extremes with offsets)
+            // (A group past K or N gives scale 0 and is not stored.  The columns of a group of up to
+            // 64 are all in or all out; in one of 128 the zeros past K could change only extremes
+            // with offsets, which leave them out.)
             float s, z = 0.0f;
             if constexpr (ZERO) {
                 float lo = in ? v[0] : kInf, hi = in ? v[0] : -kInf;
@@ -159,14 +159,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
                     const float w = ZERO ? __fsub_rn(v[column_at(b)], z) : v[column_at(b)];
-                    const float t = s > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(w, s)), -8.0f), 7.0f) : 0.0f;
-                    word |= (uint32_t)((int)t + 8) << (4 * b);
+                    const float t = fminf(fmaxf(rintf(__fdiv_rn(w, s)), -8.0f), 7.0f);
+                    word |= (uint32_t)((int)(s > 0.0f ? t : 0.0f) + 8) << (4 * b);
                 }
             }
             if (!in) word = 0x88888888u;
             if (n0 + r < N && c < C) dst[(long long)r * 16 * C] = word;
             if (l % kLanes == 0) {
-                s_scale[half % kQChunks * kPer + l / kLanes][r] = (uint16_t)(__float_as_uint(s) >> 16);
+                s_scale[half % kQChunks * kPer + l / kLanes][r] =
+                    (uint16_t)(__float_as_uint(s) >> 16);
                 if (ZERO)
                     s_zero[half % kQChunks * kPer + l / kLanes][r] =
                         (uint16_t)(__float_as_uint(z) >> 16);
@@ -196,7 +197,9 @@ struct Unpack {
     }
     __device__ __forceinline__ uint32_t pair(uint32_t word, int i) const {
         uint32_t u;
-        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(u) : "r"(word >> (4 * i)), "r"(mask), "r"(magic));
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+            : "=r"(u)
+            : "r"(word >> (4 * i)), "r"(mask), "r"(magic));
         const uint32_t k136 = 0x43084308u;
         const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u),
                                          *reinterpret_cast<const __nv_bfloat162*>(&k136));
@@ -205,7 +208,8 @@ struct Unpack {
 };
 
 // Values in bfloat16, [E, N, K], on the quantiser's tiles: a lane per word (8 columns, one 16-byte
-// store; 16 lanes write 256 bytes in a row).  Without offsets the product s (q - 8) is exact in
+// store; 16 lanes write 256 bytes in a row).  53 us for 64 x 1024 x 2048; its bytes take 52 at the copy
+// bandwidth.  Without offsets the product s (q - 8) is exact in
 // 12 bits, so the bfloat16 multiply rounds it once, like the float32 one.
 template <bool ZERO, int G>
 __global__ void __launch_bounds__(256)
@@ -283,11 +287,21 @@ __global__ void __launch_bounds__(256)
 // gives.
 //
 // The copying warps fill a ring of stages that runs ahead across units: one the weights (tensor-map
-// copies of 128-byte rows: 64-byte rows took twice as long, the copy engine moves a row in about
-// 4 cycles), one scales and rows (16-byte cp.async: bulk copies are issued lane by lane, and 20 of
-// them took longer than a step's products).  Full / empty barriers hand the stages over.  Every wait
-// is bounded; one that runs out records MOE_DEV_TIMEOUT and the block finishes without waiting any
+// copies of 128-byte rows: 64-byte rows took twice as long, the copy engine moves a row in about 4
+// cycles), one scales and rows (16-byte cp.async: bulk copies are issued lane by lane, and 20 of them
+// took longer than a step's products).  Full / empty barriers hand the stages over.  Every wait is
+// bounded; one that runs out records MOE_DEV_TIMEOUT and the block finishes without waiting any
 // more.
+//
+// Measured, 64 experts of 2048 x 1024 (134 million weights, 72 MB with scales of 64 columns), 64
+// tokens, 8 experts each: 30-33 us a product, 2.3 TB/s of weights.  What bounds it is the instructions
+// of a chunk (4096 weights): about 400, of which the unpacking takes 176 (7 of the integer unit, which
+// starts one every second cycle, and 4 of the half-precision one a word), issued at 45-50% with the 5
+// warps per scheduler that 96 registers leave room for.  The copies alone take 16 us.  On the way:
+// K split over all 8 warps with rows from global memory 78 us; group sizes as template arguments (a
+// runtime division is 30 instructions) 37; rows through the L1 cache 41; 16 product warps in one block
+// per SM 33.  Unpacking into tensor memory for tcgen05 products was tried and took 42: at 16 rows a
+// product of 16 columns takes 40 cycles, and the barriers of a 16 KB stage half a microsecond.
 // ------------------------------------------------------------------------------------------------
 enum W4Epi { kW4SiLU = 0, kW4Bias = 1, kW4SwiGLU = 2 };
 
@@ -478,7 +492,8 @@ struct W4Kernel {
             out[f + 8] = bf16_round(silu(v[1]) * v[3]);
         } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) out[f + 8 * r] = bf16_round(EPI == kW4SiLU ? silu(v[r]) : v[r]);
+            for (int r = 0; r < 4; ++r)
+                out[f + 8 * r] = bf16_round(EPI == kW4SiLU ? silu(v[r]) : v[r]);
         }
     }
 };
