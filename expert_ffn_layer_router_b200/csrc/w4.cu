@@ -52,6 +52,14 @@ __device__ __forceinline__ uint16_t bf16_round(float v) {
 constexpr float kRound = 12582920.0f;                  // 1.5 * 2^23 + 8 (even: halves stay halves)
 constexpr uint32_t kRoundBits = 0x4b400008u - 8u;      // its bits, without the 8
 
+// a / D (D = 7 or 15) rounded once, a >= 0: the same correction with the constant's reciprocal.
+template <int D>
+__device__ __forceinline__ float div_by(float a) {
+    constexpr float r = 1.0f / D;
+    const float t = __fmul_rn(a, r);
+    return a > 7.9e-31f ? __fmaf_rn(__fmaf_rn(-t, (float)D, a), r, t) : __fdiv_rn(a, (float)D);
+}
+
 template <class T>
 __device__ __forceinline__ void unpack8(const uint4 (&raw)[sizeof(T) / 2], float (&f)[8]) {
 #pragma unroll
@@ -131,7 +139,7 @@ __global__ void __launch_bounds__(256)
                     hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, h));
                 }
                 const bool any = hi >= lo;
-                s = any ? bf16_bits(bf16_round(__fdiv_rn(__fsub_rn(hi, lo), 15.0f))) : 0.0f;
+                s = any ? bf16_bits(bf16_round(div_by<15>(__fsub_rn(hi, lo)))) : 0.0f;
                 z = any ? bf16_bits(bf16_round(__fadd_rn(lo, __fmul_rn(8.0f, s)))) : 0.0f;
             } else {
                 float top = fabsf(v[0]);
@@ -140,7 +148,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
                 for (int h = 1; h < kLanes; h *= 2)
                     top = fmaxf(top, __shfl_xor_sync(kFull, top, h));
-                s = bf16_bits(bf16_round(__fdiv_rn(top, 7.0f)));
+                s = bf16_bits(bf16_round(div_by<7>(top)));
             }
             const float inv = __frcp_rn(s);
             uint32_t acc = 0;
