@@ -302,12 +302,12 @@ __global__ void __launch_bounds__(256)
 // more.
 //
 // Measured, 64 experts of 2048 x 1024 (134 million weights, 72 MB with scales of 64 columns), 64
-// tokens, 8 experts each: 30-33 us a product, 2.3 TB/s of weights.  What bounds it is the instructions
+// tokens, 8 experts each: 28-31 us a product, 2.5 TB/s of weights.  What bounds it is the instructions
 // of a chunk (4096 weights): about 400, of which the unpacking takes 176 (7 of the integer unit, which
 // starts one every second cycle, and 4 of the half-precision one a word), issued at 45-50% with the 5
 // warps per scheduler that 96 registers leave room for.  The copies alone take 16 us.  On the way:
 // K split over all 8 warps with rows from global memory 78 us; group sizes as template arguments (a
-// runtime division is 30 instructions) 37; rows through the L1 cache 41; 16 product warps in one block
+// runtime division is 30 instructions) 37; KS as one too 4-6% less, at every batch; rows through the L1 cache 41; 16 product warps in one block
 // per SM 33.  Unpacking into tensor memory for tcgen05 products was tried and took 42: at 16 rows a
 // product of 16 columns takes 40 cycles, and the barriers of a 16 KB stage half a microsecond.
 // ------------------------------------------------------------------------------------------------
@@ -326,7 +326,6 @@ struct W4Args {
     uint16_t* D;
     int ldd;
     bool early;               // the launch before this one wrote A alone: all else may start first
-    int lks;                  // log2 of KS, the warps that share a unit's K (2, 4 or 8)
     DeviceStatus* st;
 };
 
@@ -380,13 +379,16 @@ __device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v));
 // A unit's place: expert, feature block, first row of the row tile, rows in it.
 struct Unit { int e, fb, row0, rows; };
 
-template <int EPI, bool ZERO, int G>
+template <int EPI, bool ZERO, int G, int LKS>
 struct W4Kernel {
+    static constexpr int KS = 1 << LKS;           // warps that share a unit's K
+    static constexpr int UG = kWarps / KS;        // groups of 32 features of a unit
+    static constexpr int row_tile = 2 * kLines / KS;
+    static constexpr int kTiles = LKS == 1 ? 2 : 1;          // 8-row tiles of a unit
     static constexpr int kPer = 256 / G;          // groups of a box
     const W4Args& a;
     const int* s_pre;         // units before each expert
     int S, groups, nfb;       // 256-column boxes of K, groups of K, feature blocks
-    int UG, row_tile;         // 8 >> lks, 32 >> lks
 
     __device__ __forceinline__ Unit unit_at(int u) const {
         int lo = 0, hi = a.E - 1;                 // largest e with s_pre[e] <= u
@@ -395,7 +397,7 @@ struct W4Kernel {
             if (s_pre[mid] <= u) lo = mid; else hi = mid - 1;
         }
         const int r0 = a.offsets[lo], r1 = a.offsets[lo + 1];
-        const int tiles = (r1 - r0 + row_tile - 1) >> (5 - a.lks);
+        const int tiles = (r1 - r0 + row_tile - 1) / row_tile;
         const int i = u - s_pre[lo];
         Unit x;
         x.e = lo;
@@ -406,7 +408,7 @@ struct W4Kernel {
     }
     // First rows of W of the two halves of a unit's features (gated: gate rows, up rows).
     __device__ __forceinline__ int first(const Unit& u, int h) const {
-        const int half = 16 * UG;
+        constexpr int half = 16 * UG;
         if constexpr (EPI == kW4SwiGLU) return h ? a.N / 2 + u.fb * half : u.fb * half;
         return u.fb * 2 * half + h * half;
     }
@@ -417,9 +419,9 @@ struct W4Kernel {
     template <int NT>
     __device__ __forceinline__ void chunk(const uint8_t* wl,
                                           const uint8_t* sl, const uint8_t* xl,
-                                          const Unpack& unpack, float (&acc)[2][2][4]) const {
+                                          const Unpack& unpack, float (&acc)[kTiles][2][4]) const {
         // r-th feature of the lane: 8 rows on, and 16 UG rows on between gate and up.
-        const int up = EPI == kW4SwiGLU ? 16 * UG : 16;
+        constexpr int up = EPI == kW4SwiGLU ? 16 * UG : 16;
         uint4 w[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -506,7 +508,7 @@ struct W4Kernel {
     }
 };
 
-template <int EPI, bool ZERO, int G>
+template <int EPI, bool ZERO, int G, int LKS>
 __global__ void __launch_bounds__(kThreads, 2)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tm, const W4Args args) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -520,13 +522,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         reinterpret_cast<uint8_t*>(red) + kRedBytes + 2 * kStages * 8);
     int* s_pre = reinterpret_cast<int*>(s_row + kLines);
     int* s_bad = s_pre + args.E + 1;
-    W4Kernel<EPI, ZERO, G> w{args, s_pre};
-    const int KS = 1 << args.lks, NB = KS / 2;       // chunks and 256-column boxes of a step
+    using Kernel = W4Kernel<EPI, ZERO, G, LKS>;
+    constexpr int KS = Kernel::KS, UG = Kernel::UG, row_tile = Kernel::row_tile;
+    constexpr int kTiles = Kernel::kTiles, NB = KS / 2;      // (NB: 256-column boxes of a step)
+    Kernel w{args, s_pre};
     w.S = (args.K + 255) / 256;
     w.groups = (args.K + G - 1) / G;
-    w.UG = kWarps >> args.lks;
-    w.nfb = (args.N / 32 + w.UG - 1) >> (3 - args.lks);
-    w.row_tile = 2 * kLines >> args.lks;
+    w.nfb = (args.N / 32 + UG - 1) / UG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = args.E;
     if (threadIdx.x == 0) {
@@ -553,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             int n = e < E ? args.offsets[e + 1] - args.offsets[e] : 0;
             bad |= n < 0;
             n = max(n, 0);
-            const int units = ((n + w.row_tile - 1) >> (5 - args.lks)) * w.nfb;
+            const int units = (n + row_tile - 1) / row_tile * w.nfb;
             int inc = units;
 #pragma unroll
             for (int h = 1; h < 32; h *= 2) {
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) {
             int slot = 0;
             uint32_t phase = 0, issued = 0;
-            const int half = 16 * w.UG;
+            constexpr int half = 16 * UG;
             bool ok = true;
             for (int u = u0; u < u1 && ok; ++u) {
                 const Unit x = w.unit_at(u);
@@ -629,10 +631,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int u = u0; u < u1 && ok; ++u) {
             const Unit x = w.unit_at(u);
             // Rows of the lines (box line / row_tile, row line % row_tile; null: no row).
-            const bool two = args.lks > 1 || x.rows > 8;      // (else lines 8 .. 15 are not read)
+            const bool two = LKS > 1 || x.rows > 8;           // (else lines 8 .. 15 are not read)
             __syncwarp();
             if (lane < kLines) {
-                const int rr = lane & (w.row_tile - 1);
+                const int rr = lane % row_tile;
                 const uint16_t* src = nullptr;
                 if (rr < x.rows) {
                     int r = x.row0 + rr;
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                     if (r >= 0)
-                        src = args.A + (long long)r * args.K + (lane >> (5 - args.lks)) * 256;
+                        src = args.A + (long long)r * args.K + lane / row_tile * 256;
                 }
                 s_row[lane] = src;
             }
@@ -660,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // Scales: piece i of the lane belongs to group i KS + lg of the step; 8 features from
             // f (past the end: none).
-            const int lg = lane >> (5 - args.lks), piece = lane & (4 * w.UG - 1);
-            const int f = w.first(x, piece >= 2 * w.UG) + (piece & (2 * w.UG - 1)) * 8;
+            const int lg = lane / (4 * UG), piece = lane % (4 * UG);
+            const int f = w.first(x, piece >= 2 * UG) + piece % (2 * UG) * 8;
             const long long per_step = (long long)KS * args.N;
             long long side = ((long long)x.e * w.groups + lg) * args.N + f;
             int left = f < args.N ? w.groups - lg : 0;       // groups from this lane's first on
@@ -673,12 +675,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < kLines; ++i) {
                     if (i == 8 && !two) break;
-                    const bool in = ((there >> i) & 1u) && cols > (i >> (5 - args.lks)) * 256;
+                    const bool in = ((there >> i) & 1u) && cols > i / row_tile * 256;
                     cp_async_16z(dst + i * kLineBytes, line[i], in ? 16 : 0);
                     if (cols > NB * 256) line[i] += NB * 256;    // (stays inside the row)
                 }
 #pragma unroll
-                for (int i = 0; i < W4Kernel<EPI, ZERO, G>::kPer / 2; ++i) {
+                for (int i = 0; i < Kernel::kPer / 2; ++i) {
                     const bool in = left > 0;
                     const uint32_t d = dst + kStageX + 32 * i * 16;
                     cp_async_16z(d, args.scale + (in ? side : 0), in ? 16 : 0);
@@ -699,27 +701,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         return;
     }
 
-    const int g = lane >> 2, t = lane & 3, ug = warp >> args.lks, ks = warp & (KS - 1);
+    const int g = lane >> 2, t = lane & 3, ug = warp / KS, ks = warp % KS;
     const Unpack unpack;
     // This lane's places in a stage: first feature's words, its scale, its row of the first tile.
     // (With KS > 4 a box has fewer than 8 rows; lanes of the columns past them read other lines, or
     // what lies behind the last one: their sums are not used.)
     const int box = ks >> 1, h = ks & 1;
     const int frow = EPI == kW4SwiGLU ? ug * 16 + g : ug * 32 + g;
-    const int w_at = (box * 32 * w.UG + frow) * 128 + (((h * 4 + t) ^ g) << 4);
-    const int x_at = kStageW + (box * w.row_tile + g) * kLineBytes + h * 256 + t * 16;
-    const int s_at = kStageW + kStageX + (box * (256 / G) + h * (128 / G)) * 64 * w.UG + frow * 2;
+    const int w_at = (box * 32 * UG + frow) * 128 + (((h * 4 + t) ^ g) << 4);
+    const int x_at = kStageW + (box * row_tile + g) * kLineBytes + h * 256 + t * 16;
+    const int s_at = kStageW + kStageX + (box * (256 / G) + h * (128 / G)) * 64 * UG + frow * 2;
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int u = u0; u < u1; ++u) {
         const Unit x = w.unit_at(u);
-        const int nt = (x.rows + 7) / 8;
-        const int bl = x.fb * w.UG + ug;
+        const int nt = kTiles == 1 ? 1 : (x.rows + 7) / 8;
+        const int bl = x.fb * UG + ug;
         const bool feat = bl * 32 < args.N;
-        float acc[2][2][4];
+        float acc[kTiles][2][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint8_t* stage = smem + slot * kStage;
                 if (nt == 1)
                     w.template chunk<1>(stage + w_at, stage + s_at, stage + x_at, unpack, acc);
-                else
+                else if constexpr (kTiles == 2)
                     w.template chunk<2>(stage + w_at, stage + s_at, stage + x_at, unpack, acc);
             }
             __syncwarp();
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         // acc[n][m][i]: row 2 t + i % 2 of tile n, feature g + 16 m + 8 (i / 2).
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < kTiles; ++n) {
             if (n >= nt) break;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -754,9 +756,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             asm volatile("bar.sync 1, 256;" ::: "memory");
             // Thread i < 64 UG joins 4 features of a row: (group, row, g).
             const int i = threadIdx.x, jg = i >> 6, row = (i >> 3) & 7, fg = i & 7;
-            const int jb = x.fb * w.UG + jg;
-            if (ok && jg < w.UG && n * 8 + row < x.rows && jb * 32 < args.N) {
-                const float* s = red + ((jg << args.lks) * 8 + row) * kRedStride + fg;
+            const int jb = x.fb * UG + jg;
+            if (ok && jg < UG && n * 8 + row < x.rows && jb * 32 < args.N) {
+                const float* s = red + (jg * KS * 8 + row) * kRedStride + fg;
                 float v[4] = {s[0], s[8], s[16], s[24]};
                 for (int q = 1; q < KS; ++q)
 #pragma unroll
@@ -768,30 +770,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-template <int EPI, bool ZERO, int G>
+template <int EPI, bool ZERO, int G, int LKS>
 cudaError_t run_w4(const CUtensorMap& tm, const W4Args& a, cudaStream_t s) {
-    auto kern = w4_gemm_kernel<EPI, ZERO, G>;
+    auto kern = w4_gemm_kernel<EPI, ZERO, G, LKS>;
     const int smem = w4_smem_bytes<ZERO, G>(a.E);
     static std::atomic<int> allowed[64];
     const cudaError_t e = allow_smem(kern, allowed, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(2 * kSm), dim3(kThreads), smem, s, tm, a);
 }
-
-template <int EPI>
-cudaError_t run_w4(const CUtensorMap& tm, const W4Args& a, int G, cudaStream_t s) {
-    if (a.zero)
-        return G == 32   ? run_w4<EPI, true, 32>(tm, a, s)
-               : G == 64 ? run_w4<EPI, true, 64>(tm, a, s)
-                         : run_w4<EPI, true, 128>(tm, a, s);
-    return G == 32   ? run_w4<EPI, false, 32>(tm, a, s)
-           : G == 64 ? run_w4<EPI, false, 64>(tm, a, s)
-                     : run_w4<EPI, false, 128>(tm, a, s);
-}
-
-}  // namespace
-
-namespace {
 
 // Calls f(first expert, experts, grid) for the tiles of E experts: row tiles on y (at most 65535 a
 // launch), chunks on x.
@@ -863,23 +850,33 @@ cudaError_t launch_w4_gemm(int which, const void* A, const int32_t* a_rows, int 
                            const float* bias, void* D, int ldd, DeviceStatus* st, cudaStream_t s,
                            int* launches) {
     W4Args a{(const uint16_t*)A, a_rows, a_row_limit, offsets, E, K, N, max_rows, scale, zero,
-             bias, (uint16_t*)D, ldd, a_rows == nullptr, 1, st};
+             bias, (uint16_t*)D, ldd, a_rows == nullptr, st};
     // Warps that share a unit's K: the fewest that give every SM a unit, at most 8 and no more than
     // there are chunks.  (Both products, 64 experts of 2048 x 1024, KS = 2, 4, 8: 1 token 22, 17,
     // 16 us; 2 tokens 23, 20, 23; 4 tokens 29, 30, 33; 64 tokens 64, 77, 152.)
-    while (a.lks < 3 && (256 << a.lks) <= K &&
-           (long long)std::min(E, max_rows) * (N / 32) < (long long)kSm * (kWarps >> a.lks))
-        a.lks += 1;
+    int lks = 1;
+    while (lks < 3 && (256 << lks) <= K &&
+           (long long)std::min(E, max_rows) * (N / 32) < (long long)kSm * (kWarps >> lks))
+        lks += 1;
     // Words as 16-bit pairs: boxes of 128 bytes (256 columns) x 16 UG rows.
     const int cols = 32 * ((K + 127) / 128);
     CUtensorMap tm;
-    if (!make_tmap_2d(&tm, q, (long long)E * N, cols, cols, 64, 16 * (kWarps >> a.lks),
+    if (!make_tmap_2d(&tm, q, (long long)E * N, cols, cols, 64, 16 * (kWarps >> lks),
                       CU_TENSOR_MAP_SWIZZLE_128B))
         return note_launch(cudaErrorInvalidValue);
-    cudaError_t e;
-    if (which == kW4SiLU) e = run_w4<kW4SiLU>(tm, a, G, s);
-    else if (which == kW4Bias) e = run_w4<kW4Bias>(tm, a, G, s);
-    else e = run_w4<kW4SwiGLU>(tm, a, G, s);
+    cudaError_t e = cudaSuccess;
+    w4_format(zero != nullptr, G, [&](auto z, auto g) {
+        auto with = [&](auto epi) {
+            constexpr int EPI = decltype(epi)::value, kG = decltype(g)::value;
+            constexpr bool Z = decltype(z)::value;
+            e = lks == 1   ? run_w4<EPI, Z, kG, 1>(tm, a, s)
+                : lks == 2 ? run_w4<EPI, Z, kG, 2>(tm, a, s)
+                           : run_w4<EPI, Z, kG, 3>(tm, a, s);
+        };
+        if (which == kW4SiLU) with(std::integral_constant<int, kW4SiLU>());
+        else if (which == kW4Bias) with(std::integral_constant<int, kW4Bias>());
+        else with(std::integral_constant<int, kW4SwiGLU>());
+    });
     *launches += 1;
     return e;
 }
