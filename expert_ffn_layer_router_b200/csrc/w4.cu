@@ -307,9 +307,10 @@ __global__ void __launch_bounds__(256)
 // starts one every second cycle, and 4 of the half-precision one a word), issued at 45-50% with the 5
 // warps per scheduler that 96 registers leave room for.  The copies alone take 16 us.  On the way:
 // K split over all 8 warps with rows from global memory 78 us; group sizes as template arguments (a
-// runtime division is 30 instructions) 37; KS as one too 4-6% less, at every batch; rows through the L1 cache 41; 16 product warps in one block
-// per SM 33.  Unpacking into tensor memory for tcgen05 products was tried and took 42: at 16 rows a
-// product of 16 columns takes 40 cycles, and the barriers of a 16 KB stage half a microsecond.
+// runtime division is 30 instructions) 37; rows through the L1 cache 41; 16 product warps in one block
+// per SM 33; KS as a template argument too: 4-6% less at every batch.  Unpacking into tensor memory
+// for tcgen05 products was tried and took 42: at 16 rows a product of 16 columns takes 40 cycles, and
+// the barriers of a 16 KB stage half a microsecond.
 // ------------------------------------------------------------------------------------------------
 enum W4Epi { kW4SiLU = 0, kW4Bias = 1, kW4SwiGLU = 2 };
 
