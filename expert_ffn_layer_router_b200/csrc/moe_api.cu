@@ -201,10 +201,19 @@ bool bad_w4(const moe_w4* w) {
            misaligned(w->scale, 16) || misaligned(w->zero, 16);
 }
 
-// Rows of a 4-bit weight are addressed by 32-bit numbers in the copies' tensor maps.
+constexpr int32_t kW4MaxRows = 32 * 65535;    // row tiles of 32 on one grid axis
+constexpr int32_t kW4MaxCols = 1 << 30;       // columns are counted in 32 bits
+
+bool bad_w4_shape(int32_t E, int32_t N, int32_t K) {
+    return K % 64 != 0 || K > kW4MaxCols || N > kW4MaxRows || E > 65535;
+}
+
+// Rows of a 4-bit weight, within an expert as above (reading back) and in all: they are addressed
+// by 32-bit numbers in the copies' tensor maps.
 bool w4_too_many_rows(const moe_problem* p) {
     const long long n1 = (p->flags & MOE_FLAG_GATED) ? 2LL * p->d_ff : p->d_ff;
-    return (long long)p->E * std::max<long long>(n1, p->d_model) > 0x7fffffffLL;
+    const long long n = std::max<long long>(n1, p->d_model);
+    return n > kW4MaxRows || p->E * n > 0x7fffffffLL;
 }
 
 int w4_rows1(const moe_problem* p) {          // rows of W1 per expert
@@ -220,8 +229,6 @@ constexpr long long kW4DirectRows = 64;
 bool w4_direct(const moe_problem* p) {
     return max_rows_of(p, capacity_of(p)) <= kW4DirectRows * p->E;
 }
-
-constexpr int32_t kW4MaxRows = 32 * 65535;    // row tiles of 32 on one grid axis
 
 // bfloat16 copy of one of the two weights (they are used one after the other).
 size_t w4_copy_bytes(const moe_problem* p) {
@@ -664,7 +671,7 @@ moe_status moe_quantize_packed(const void* W, int32_t dtype, int32_t E, int32_t 
                            int32_t group, void* q, void* scale, void* zero, void* stream) {
     if ((dtype != MOE_F32 && dtype != MOE_BF16) || E < 1 || N < 1 || K < 1 || bad_group(group))
         return MOE_ERR_INVALID_ARG;
-    if (K % 64 != 0 || N > kW4MaxRows || E > 65535) return MOE_ERR_UNSUPPORTED;
+    if (bad_w4_shape(E, N, K)) return MOE_ERR_UNSUPPORTED;
     if (!W || !q || !scale || misaligned(W, 16) || misaligned(q, 16) || misaligned(scale, 16) ||
         misaligned(zero, 16))
         return MOE_ERR_INVALID_ARG;
@@ -679,7 +686,7 @@ moe_status moe_quantize_packed(const void* W, int32_t dtype, int32_t E, int32_t 
 moe_status moe_dequantize_packed(const moe_w4* w, int32_t E, int32_t N, int32_t K, void* W,
                              void* stream) {
     if (bad_w4(w) || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-    if (K % 64 != 0 || N > kW4MaxRows || E > 65535) return MOE_ERR_UNSUPPORTED;
+    if (bad_w4_shape(E, N, K)) return MOE_ERR_UNSUPPORTED;
     if (!W || misaligned(W, 16)) return MOE_ERR_INVALID_ARG;
     cudaGetLastError();
     moe::g_launch_error = cudaSuccess;

@@ -236,11 +236,12 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
                        size_t ws_bytes, void* stream);
 
 /* ---- 4-bit expert weights ------------------------------------------------------------------
- * Quantises W [E, N, K] (dtype MOE_BF16 or MOE_F32, dense, finite, 16-byte aligned) to the format
- * of moe_w4.  Per group, zero = NULL: scale = max|w| / 7; else scale = (max - min) / 15 and zero =
+ * Quantises W [E, N, K] (dtype MOE_BF16 or MOE_F32, dense, 16-byte aligned; values finite, below
+ * 2^126 in magnitude) to the format of moe_w4.  Per group, zero = NULL: scale = max|w| / 7; else scale = (max - min) / 15 and zero =
  * min + 8 scale.  Both are rounded to bfloat16 first (the divisions and sums in float32), then
  * nibble - 8 = round-half-even((w - zero) / scale), clamped to [-8, 7]; 0 where scale = 0.
- * K must be a multiple of 64 and N at most 2097120 (else MOE_ERR_UNSUPPORTED). */
+ * K must be a multiple of 64 and at most 2^30, N at most 2097120 and E at most 65535 (else
+ * MOE_ERR_UNSUPPORTED). */
 moe_status moe_quantize_packed(const void* W, int32_t dtype, int32_t E, int32_t N, int32_t K,
                            int32_t group, void* q, void* scale, void* zero, void* stream);
 
@@ -255,8 +256,9 @@ moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes);
 
 /* moe_expert_ffn over 4-bit weights: W1 is [E, d_ff, d_model] ([E, 2 d_ff, d_model] with
  * MOE_FLAG_GATED), W2 [E, d_model, d_ff]; their groups may differ.  p's dtype is MOE_BF16 (else
- * MOE_ERR_UNSUPPORTED), with moe_expert_ffn's rules for widths, alignment, offsets and rowtok; rows
- * of Y behind offsets[E] are left as they were.
+ * MOE_ERR_UNSUPPORTED; so are weights of over 2097120 rows an expert or 2^31 - 1 in all), with
+ * moe_expert_ffn's rules for widths, alignment, offsets and rowtok; rows of Y behind offsets[E] are
+ * left as they were.
  * Few rows per expert (min(T k, E K) <= 64 E): the products read the 4-bit weights and form
  * sum_k (nibble - 8) x_k per group exactly in float32 before the scale; b1, b2 nullable.  More rows:
  * each weight is first read back to bfloat16 (one rounding per value) into the workspace, for the

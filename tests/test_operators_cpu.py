@@ -166,3 +166,26 @@ def test_workspace_sizes(moe):
     assert L.moe_workspace_size_packed(prob(moe, dtype=0), ctypes.byref(n)) == 2
     assert L.moe_workspace_size_packed(prob(moe, d=96), ctypes.byref(n)) == 2
     assert L.moe_workspace_size_packed(prob(moe), None) == 1
+
+
+def test_packed_weight_size_limits(moe):
+    """Sizes past what the tiles of a weight are counted in are refused, in every call that would
+    walk them."""
+    L, n = moe.lib(), ctypes.c_size_t()
+    w = ctypes.byref(moe.W4(1 << 20, 1 << 20, None, 64))
+    rows, cols = 32 * 65535, 1 << 30
+    assert L.moe_quantize_packed(FAKE, 1, 1, 32, cols + 64, 64, FAKE, FAKE, None, None) == 2
+    assert L.moe_quantize_packed(FAKE, 1, 65536, 32, 64, 64, FAKE, FAKE, None, None) == 2
+    assert L.moe_dequantize_packed(w, 1, 32, cols + 64, FAKE, None) == 2
+    assert L.moe_dequantize_packed(w, 1, rows + 1, 64, FAKE, None) == 2
+    for size in (dict(F=rows + 32), dict(d=rows + 32), dict(F=(rows + 64) // 2, flags=4)):
+        for T in (16, 4096):                         # (directly; after reading back)
+            a = dict(T=T, E=1, k=1)
+            a.update(size)
+            a = {key: -(-v // 128) * 128 if key in "dF" else v for key, v in a.items()}
+            p = prob(moe, **a)
+            assert L.moe_workspace_size_packed(p, ctypes.byref(n)) == 2
+            assert L.moe_expert_ffn_packed(p, FAKE, FAKE, FAKE, w, None, w, None, FAKE, FAKE, BIG,
+                                           None) == 2
+            assert L.moe_forward_block(p, FAKE, None, FAKE, None, None, None, w, w, None, None,
+                                       FAKE2, *[None] * 6, FAKE, BIG, None) == 2
