@@ -146,10 +146,11 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
     return v;
 }
 
-// 1 / sqrt(a), a >= 0: the approximation and one step of Newton's iteration on y^-2 = a.
+// 1 / sqrt(a), a >= 0: the approximation and one step of Newton's iteration on y^-2 = a (not for 0
+// and infinity, where the step would make a NaN of inf 0).
 __device__ __forceinline__ float inv_sqrt(float a) {
     const float y = rsqrtf(a);
-    return a > 0.0f ? y * fmaf(-0.5f * a * y, y, 1.5f) : y;
+    return a > 0.0f && y > 0.0f ? y * fmaf(-0.5f * a * y, y, 1.5f) : y;
 }
 
 template <int WPR>

@@ -272,7 +272,7 @@ moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int3
  * y = gamma (x - mean) rstd + beta per token, rstd = 1 / sqrt(variance + eps), the variance over
  * d_model without bias correction.  x, y [T, d_model] in p's dtype, any d_model; gamma, beta
  * [d_model] float32; mean, rstd [T] float32 out.  eps >= 0 and finite (with eps = 0 a row of equal
- * values gives NaN); d_model at most 2^30.  y must not alias x.  Statistics are float32, y is
+ * values gives NaN; where a float32 variance overflows, rstd is 0 and y is beta); d_model at most 2^30.  y must not alias x.  Statistics are float32, y is
  * rounded once. */
 moe_status moe_layer_norm(const moe_problem* p, const void* x, const float* gamma,
                           const float* beta, float eps, void* y, float* mean, float* rstd,

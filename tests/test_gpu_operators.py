@@ -363,6 +363,28 @@ def test_layer_norm_hard_rows(moe):
         assert torch.equal(y[0], beta.to(DT[dtype]))
 
 
+@pytest.mark.parametrize("d", [60, 768, 8200])
+def test_layer_norm_variance_overflow(moe, d):
+    """A row whose variance passes float32's range: rstd 0, y = beta and dx = dres, at every width;
+    the other rows do not see it."""
+    T = 5
+    g = gen(d)
+    for dtype in ("bf16", "f32"):
+        x = randn(g, T, d)
+        x[2] *= 1e25
+        x = x.to(DT[dtype])
+        gamma, beta = randn(g, d), randn(g, d)
+        dy, dres = randn(g, T, d).to(DT[dtype]), randn(g, T, d).to(DT[dtype])
+        layer = moe.MoELayer(T, d, 64, 1, 1, dtype=dtype)
+        y, mean, rstd = layer.layer_norm(x, gamma, beta)
+        assert rstd[2] == 0 and torch.equal(y[2], beta.to(DT[dtype]))
+        dx, dg, db = layer.layer_norm_backward(dy, x, gamma, mean, rstd, dres)
+        assert torch.equal(dx[2], dres[2]) and torch.isfinite(dg).all() and torch.isfinite(db).all()
+        keep = torch.tensor([0, 1, 3, 4], device=dev())
+        rest = moe.MoELayer(4, d, 64, 1, 1, dtype=dtype).layer_norm(x[keep], gamma, beta)
+        assert torch.equal(y[keep], rest[0]) and torch.equal(rstd[keep], rest[2])
+
+
 def test_layer_norm_unaligned_and_no_rows(moe):
     """Pointers off the 16-byte boundary take the one-element loads; T = 0 clears the sums."""
     T, d = 20, 512
