@@ -347,6 +347,8 @@ class _on:
 
     def __enter__(self):
         index = self.device.index
+        if self.device.type != "cuda":
+            raise MoeError(MOE_ERR_INVALID_ARG, "tensors must be on a CUDA device, not on %s" % self.device)
         if self.stream is None and index == torch._C._cuda_getDevice():
             return torch._C._cuda_getCurrentRawStream(index)
         guards = [torch.cuda.device(self.device)]

@@ -189,3 +189,24 @@ def test_packed_weight_size_limits(moe):
                                            None) == 2
             assert L.moe_forward_block(p, FAKE, None, FAKE, None, None, None, w, w, None, None,
                                        FAKE2, *[None] * 6, FAKE, BIG, None) == 2
+
+
+def test_cpu_tensors_are_refused(moe):
+    """Tensors in host memory never reach a kernel."""
+    import torch
+    w = moe.W4Weights(torch.zeros(4, 64, 16, dtype=torch.int32),
+                      torch.zeros(4, 1, 64, dtype=torch.bfloat16), K=64, group=64)
+    x, f = torch.zeros(16, 64, dtype=torch.bfloat16), torch.zeros(64)
+    ids, logits = torch.zeros(16, 2, dtype=torch.int32), torch.zeros(16, 4)
+    rows, counts = torch.zeros(32, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    layer = moe.MoELayer(16, 64, 64, 4, 2, device="cpu", w4=True)
+    m = torch.zeros(16)
+    for call in (lambda: moe.quantize_w4(torch.zeros(1, 32, 64), 32), lambda: moe.dequantize_w4(w),
+                 lambda: layer.balance_loss(logits, ids),
+                 lambda: layer.route_backward(logits, ids, grad_w=torch.zeros(16, 2)),
+                 lambda: layer.layer_norm(x, f, f),
+                 lambda: layer.layer_norm_backward(x, x, f, m, m),
+                 lambda: layer.expert_ffn_w4(x, counts, rows, w, None, w, None),
+                 lambda: layer.forward_block(x, torch.zeros(64, 4), None, w, None, w, None)):
+        with pytest.raises(moe.MoeError, match="CUDA device"):
+            call()
