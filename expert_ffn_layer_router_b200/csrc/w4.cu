@@ -35,10 +35,11 @@ __device__ __forceinline__ uint16_t bf16_round(float v) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Quantising: per group, without offsets s = bf16(max|w| / 7); with offsets s = bf16((max - min) /
-// 15) and z = bf16(min + 8 s).  q - 8 = round-half-even((w - z) / s) clamped to [-8, 7], 0 where
-// s = 0.  The rounding of s and z to bfloat16 (they are what is kept) comes before the division,
-// so it costs at most half a step more.
+// Quantising: per group, without offsets s = bf16(max|w| * f32(1/7)); with offsets s = bf16((max -
+// min) * f32(1/15)) and z = bf16(min + 8 s).  (Products with the float32 reciprocal, which is how
+// float32 tensors are divided by a number elsewhere, so scales made there agree bit for bit.)  q - 8 =
+// round-half-even((w - z) / s) clamped to [-8, 7], 0 where s = 0.  The rounding of s and z to
+// bfloat16 (they are what is kept) comes before the division, so it costs at most half a step more.
 //
 // The quotients.  With i = 1 / s rounded once and t = w i, the corrected t + (w - t s) i (two fused
 // steps) is the correctly rounded quotient (P. Markstein, "Computation of elementary functions on the
@@ -46,19 +47,11 @@ __device__ __forceinline__ uint16_t bf16_round(float v) {
 // reciprocal or the remainder leaves the normal range, a thread divides.  Adding 1.5 * 2^23 + 8
 // rounds t half to even and leaves q in the low bits; the eight words of bits are joined as
 // acc = 16 acc + bits modulo 2^32, and the constant's share is taken off at the end.
-// (64 x 1024 x 2048 from bfloat16, 0.34 GB moved: 96 us, 52 at the copy bandwidth; issue-bound.  With a
+// (64 x 1024 x 2048 from bfloat16, 0.34 GB moved: 90 us, 52 at the copy bandwidth; issue-bound.  With a
 // division near halves 143 us, half of the warps meeting one.)
 // ------------------------------------------------------------------------------------------------
 constexpr float kRound = 12582920.0f;                  // 1.5 * 2^23 + 8 (even: halves stay halves)
 constexpr uint32_t kRoundBits = 0x4b400008u - 8u;      // its bits, without the 8
-
-// a / D (D = 7 or 15) rounded once, a >= 0: the same correction with the constant's reciprocal.
-template <int D>
-__device__ __forceinline__ float div_by(float a) {
-    constexpr float r = 1.0f / D;
-    const float t = __fmul_rn(a, r);
-    return a > 7.9e-31f ? __fmaf_rn(__fmaf_rn(-t, (float)D, a), r, t) : __fdiv_rn(a, (float)D);
-}
 
 template <class T>
 __device__ __forceinline__ void unpack8(const uint4 (&raw)[sizeof(T) / 2], float (&f)[8]) {
@@ -139,7 +132,7 @@ __global__ void __launch_bounds__(256)
                     hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, h));
                 }
                 const bool any = hi >= lo;
-                s = any ? bf16_bits(bf16_round(div_by<15>(__fsub_rn(hi, lo)))) : 0.0f;
+                s = any ? bf16_bits(bf16_round(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f))) : 0.0f;
                 z = any ? bf16_bits(bf16_round(__fadd_rn(lo, __fmul_rn(8.0f, s)))) : 0.0f;
             } else {
                 float top = fabsf(v[0]);
@@ -148,7 +141,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
                 for (int h = 1; h < kLanes; h *= 2)
                     top = fmaxf(top, __shfl_xor_sync(kFull, top, h));
-                s = bf16_bits(bf16_round(div_by<7>(top)));
+                s = bf16_bits(bf16_round(__fmul_rn(top, 1.0f / 7.0f)));
             }
             const float inv = __frcp_rn(s);
             uint32_t acc = 0;

@@ -237,8 +237,9 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
 
 /* ---- 4-bit expert weights ------------------------------------------------------------------
  * Quantises W [E, N, K] (dtype MOE_BF16 or MOE_F32, dense, 16-byte aligned; values finite, below
- * 2^126 in magnitude) to the format of moe_w4.  Per group, zero = NULL: scale = max|w| / 7; else scale = (max - min) / 15 and zero =
- * min + 8 scale.  Both are rounded to bfloat16 first (the divisions and sums in float32), then
+ * 2^126 in magnitude) to the format of moe_w4.  Per group, zero = NULL: scale = max|w| / 7; else
+ * scale = (max - min) / 15 and zero = min + 8 scale.  Both are rounded to bfloat16 first (the
+ * differences, products with the float32 reciprocal of 7 or 15, and sums in float32), then
  * nibble - 8 = round-half-even((w - zero) / scale), clamped to [-8, 7]; 0 where scale = 0.
  * K must be a multiple of 64 and at most 2^30, N at most 2097120 and E at most 65535 (else
  * MOE_ERR_UNSUPPORTED). */

@@ -434,8 +434,8 @@ def test_layer_norm_gradient_against_differences(moe):
 # 4-bit weights
 # ----------------------------------------------------------------------------------------------
 def quantize_reference(W, group, zeros):
-    """(nibbles - 8, scale, zero) as [E, N, K], [E, G, N]: the definition in float32 steps (torch
-    divides a CUDA tensor by a number through its reciprocal, so divisors are tensors here)."""
+    """(nibbles - 8, scale, zero) as [E, N, K], [E, G, N]: the definition in float32 steps
+    (7 and 15 through their float32 reciprocals)."""
     E, N, K = W.shape
     w = W.float()
     q, scale, zero = torch.empty_like(w), [], []
@@ -443,11 +443,11 @@ def quantize_reference(W, group, zeros):
         v = w[:, :, k0:k0 + group]
         if zeros:
             lo, hi = v.amin(2), v.amax(2)
-            s = ((hi - lo) / torch.full_like(lo, 15.0)).to(torch.bfloat16).float()
+            s = ((hi - lo) * torch.tensor(1.0 / 15.0, device=dev())).to(torch.bfloat16).float()
             z = (lo + 8.0 * s).to(torch.bfloat16).float()
         else:
             m = v.abs().amax(2)
-            s = (m / torch.full_like(m, 7.0)).to(torch.bfloat16).float()
+            s = (m * torch.tensor(1.0 / 7.0, device=dev())).to(torch.bfloat16).float()
             z = torch.zeros_like(s)
         t = torch.round((v - z[..., None]) / s[..., None]).clamp(-8, 7)
         q[:, :, k0:k0 + group] = torch.where(s[..., None] > 0, t, torch.zeros_like(t))
