@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (e < E) {
                 const int n = args.offsets ? __ldg(args.offsets + e + 1) - __ldg(args.offsets + e)
                                            : args.rows0;
-                bad |= n < 0;
+                if (args.offsets)                  // (compared: the difference may wrap)
+                    bad |= __ldg(args.offsets + e + 1) < __ldg(args.offsets + e);
                 loc += (max(n, 0) + TM - 1) / TM;
             }
         }

@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(256)
 // warps per scheduler that 96 registers leave room for.  The copies alone take 16 us.  On the way:
 // K split over all 8 warps with rows from global memory 78 us; group sizes as template arguments (a
 // runtime division is 30 instructions) 37; rows through the L1 cache 41; 16 product warps in one block
-// per SM 33; KS as a template argument too: 4-6% less at every batch.  Unpacking into tensor memory
-// for tcgen05 products was tried and took 42: at 16 rows a product of 16 columns takes 40 cycles, and
-// the barriers of a 16 KB stage half a microsecond.
+// per SM 33; KS as a template argument too: 4-6% less at every batch; a unit's offsets from shared
+// memory: 1-3% less.  Unpacking into tensor memory for tcgen05 products was tried and took 42: at 16
+// rows a product of 16 columns takes 40 cycles, and the barriers of a 16 KB stage half a microsecond.
 // ------------------------------------------------------------------------------------------------
 enum W4Epi { kW4SiLU = 0, kW4Bias = 1, kW4SwiGLU = 2 };
 
@@ -339,11 +339,12 @@ constexpr int kSideBytes = 256 * (256 / G);
 template <bool ZERO, int G>
 constexpr int kStageBytes =
     kStageW + kStageX + ((ZERO ? 2 : 1) * kSideBytes<G> + 1023) / 1024 * 1024;
-// (1024 bytes to align the ring; row pointers of the unit being copied; 2 flags)
+// (1024 bytes to align the ring; row pointers of the unit being copied; the list of units and the
+// offsets; a flag)
 template <bool ZERO, int G>
 constexpr int w4_smem_bytes(int E) {
     return 1024 + kStages * kStageBytes<ZERO, G> + kRedBytes + 2 * kStages * 8 + kLines * 8 +
-           (E + 2) * 4;
+           (2 * E + 3) * 4;
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -382,6 +383,7 @@ struct W4Kernel {
     static constexpr int kPer = 256 / G;          // groups of a box
     const W4Args& a;
     const int* s_pre;         // units before each expert
+    const int* s_off;         // the offsets
     int S, groups, nfb;       // 256-column boxes of K, groups of K, feature blocks
 
     __device__ __forceinline__ Unit unit_at(int u) const {
@@ -390,7 +392,7 @@ struct W4Kernel {
             const int mid = (lo + hi + 1) >> 1;
             if (s_pre[mid] <= u) lo = mid; else hi = mid - 1;
         }
-        const int r0 = a.offsets[lo], r1 = a.offsets[lo + 1];
+        const int r0 = s_off[lo], r1 = s_off[lo + 1];
         const int tiles = (r1 - r0 + row_tile - 1) / row_tile;
         const int i = u - s_pre[lo];
         Unit x;
@@ -515,11 +517,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint16_t** s_row = reinterpret_cast<const uint16_t**>(
         reinterpret_cast<uint8_t*>(red) + kRedBytes + 2 * kStages * 8);
     int* s_pre = reinterpret_cast<int*>(s_row + kLines);
-    int* s_bad = s_pre + args.E + 1;
+    int* s_off = s_pre + args.E + 1;
+    int* s_bad = s_off + args.E + 1;
     using Kernel = W4Kernel<EPI, ZERO, G, LKS>;
     constexpr int KS = Kernel::KS, UG = Kernel::UG, row_tile = Kernel::row_tile;
     constexpr int kTiles = Kernel::kTiles, NB = KS / 2;      // (NB: 256-column boxes of a step)
-    Kernel w{args, s_pre};
+    Kernel w{args, s_pre, s_off};
     w.S = (args.K + 255) / 256;
     w.groups = (args.K + G - 1) / G;
     w.nfb = (args.N / 32 + UG - 1) / UG;
@@ -546,9 +549,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             bad = args.offsets[0] != 0 || args.offsets[E] > args.max_rows;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            int n = e < E ? args.offsets[e + 1] - args.offsets[e] : 0;
-            bad |= n < 0;
-            n = max(n, 0);
+            const int r0 = args.offsets[min(e, E)], r1 = args.offsets[min(e + 1, E)];
+            if (e <= E) s_off[e] = r0;
+            bad |= r1 < r0;                              // (their difference may wrap)
+            const int n = max(r1 - r0, 0);
             const int units = (n + row_tile - 1) / row_tile * w.nfb;
             int inc = units;
 #pragma unroll
@@ -562,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         bad = __any_sync(kFull, bad);
         if (lane == 0) {
             s_pre[E] = total;
+            s_off[E] = args.offsets[E];
             *s_bad = bad;
             if (bad && blockIdx.x == 0) report(args.st, MOE_DEV_BAD_INDEX, 710);
         }

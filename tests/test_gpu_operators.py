@@ -687,6 +687,26 @@ def test_expert_ffn_w4_bad_offsets_and_rows(moe):
     assert_within(Y, ref, tol, "rows with a bad index")
 
 
+@pytest.mark.parametrize("T", [32, 300])                # read directly; read back first
+def test_expert_ffn_w4_offsets_whose_difference_wraps(moe, T):
+    """Offsets 2^31 apart and more are seen to decrease: nothing is read or written.  (After the
+    check of the order, an expert of a wrapped row count has no rows.)"""
+    d, F, E, k = 128, 64, 4, 2
+    g = gen(12)
+    W1, W2 = make_experts(moe, g, E, F, F, d, (32, 32), False)
+    x = randn(g, T, d).to(torch.bfloat16)
+    offsets, rowtok = routing(g, T, E, k, "random")
+    layer = moe.MoELayer(T, d, F, E, k, w4=True)
+    for inner in ((2000000000, -2000000000, 5), (2 ** 31 - 1, -2 ** 31, 0)):
+        bad = offsets.clone()
+        bad[1:4] = torch.tensor(inner, dtype=torch.int32)
+        Y = torch.full((T * k, d), 5.0, dtype=torch.bfloat16, device=dev())
+        moe.moe_expert_ffn_packed(layer.p, x, bad, rowtok, W1.c, None, W2.c, None, Y, layer.ws)
+        assert status(moe, layer) == moe.DEV_BAD_INDEX
+        assert (Y == 5.0).all()
+        moe.moe_reset_device_status(layer.ws)
+
+
 def test_expert_ffn_w4_infinities_stay_in_their_rows(moe):
     T, d, F, E, k = 16, 256, 128, 2, 1
     g = gen(12)
