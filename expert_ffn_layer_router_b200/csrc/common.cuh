@@ -12,8 +12,8 @@ namespace moe {
 
 // Workspace header: the first 256 bytes of every workspace.
 struct DeviceStatus {
-    int32_t code;      // MOE_DEV_*; first error wins
-    int32_t where;     // kernel-specific detail of the first error
+    int32_t code;      // MOE_DEV_*; first error wins, but a timeout replaces a bad index
+    int32_t where;     // kernel-specific detail of that error
 };
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;   // a pipeline wait gives up after ~2 s
@@ -26,6 +26,11 @@ __device__ __forceinline__ uint64_t global_ns() {
 
 __device__ __forceinline__ void report(DeviceStatus* st, int code, int where) {
     if (st && atomicCAS(&st->code, 0, code) == 0) st->where = where;
+}
+
+// A wait gave up: work is left out, which is more than a bad index costs, so it replaces one.
+__device__ __forceinline__ void report_timeout(DeviceStatus* st, int where) {
+    if (st && atomicExch(&st->code, MOE_DEV_TIMEOUT) != MOE_DEV_TIMEOUT) st->where = where;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -72,9 +77,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for the phase of parity `parity` to complete.  Gives up after kWaitLimitNs, or once
-// another thread has recorded an error, and then returns false after recording a timeout.  The
-// status word and the clock are read only every 32nd retry, so that a waiting thread is back in
+// Waits for the phase of parity `parity` to complete.  Gives up after kWaitLimitNs, recording a
+// timeout, or once another wait has recorded one, and then returns false.  (A bad index is an error
+// of the data: it stops no thread, every phase still completes, and the rows beside it are valid.)
+// The status word and the clock are read only every 32nd retry, so that a waiting thread is back in
 // try_wait (not in a global load) when the phase completes.
 template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, DeviceStatus* st,
@@ -84,9 +90,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, DeviceS
     for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait<kCluster>(bar, parity)) return true;
         if ((n & 31u) == 0) {
-            if (*reinterpret_cast<volatile int32_t*>(&st->code) != 0) return false;
+            if (*reinterpret_cast<volatile int32_t*>(&st->code) == MOE_DEV_TIMEOUT) return false;
             if (global_ns() - t0 > limit_ns) {
-                report(st, MOE_DEV_TIMEOUT, where);
+                report_timeout(st, where);
                 return false;
             }
         }

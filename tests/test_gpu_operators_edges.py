@@ -1,0 +1,54 @@
+"""The operators around the layer at their edges: after errors of the data, at extreme values, over
+every split of the 4-bit products, beside each other on threads.  (Helpers and bounds are those of the
+operators' main tests.)"""
+import math
+
+import pytest
+import torch
+
+from tests.gpu_util import dev
+from tests.test_gpu_operators import gen, make_experts, moe, randn, routing, status  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------------------------
+# What an error of the data leaves alone
+# ----------------------------------------------------------------------------------------------
+def test_waits_go_on_after_a_bad_index(moe):
+    """A recorded bad index ends no wait: one that nothing arrives on still runs for its limit, and
+    its timeout replaces the index error; a later index error does not replace the timeout."""
+    layer = moe.MoELayer(40, 64, 64, 4, 2)
+    logits, ids = randn(gen(1), 40, 4), torch.zeros(40, 2, dtype=torch.int32, device=dev())
+    ids[3, 1] = 4
+    layer.balance_loss(logits, ids)
+    assert status(moe, layer) == moe.DEV_BAD_INDEX
+    moe.moe_selftest_wait_timeout(layer.ws, 20000)
+    assert status(moe, layer) == moe.DEV_TIMEOUT
+    layer.balance_loss(logits, ids)
+    assert status(moe, layer) == moe.DEV_TIMEOUT
+
+
+@pytest.mark.parametrize("T", [64, 1024])                # read directly; read back first
+def test_expert_ffn_w4_after_a_bad_index(moe, T):
+    """A status word that already holds a bad index (here the router losses') and one bad row do not
+    cost any other row."""
+    d, F, E, k = 2048, 1024, 64, 8
+    g = gen(61)
+    W1, W2 = make_experts(moe, g, E, F, F, d, (64, 64), False)
+    x = randn(g, T, d).to(torch.bfloat16)
+    offsets, rowtok = routing(g, T, E, k, "random")
+    layer = moe.MoELayer(T, d, F, E, k, w4=True)
+    clean = layer.expert_ffn_w4(x, offsets, rowtok, W1, None, W2, None)
+    logits = randn(g, T, E)
+    ids = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+    ids[3, 1] = E
+    layer.balance_loss(logits, ids)
+    assert status(moe, layer) == moe.DEV_BAD_INDEX
+    bad = rowtok.clone()
+    bad[77] = T
+    rest = torch.arange(T * k, device=dev()) != 77
+    for _ in range(20):
+        Y = torch.full_like(clean, 7.0)
+        moe.moe_expert_ffn_packed(layer.p, x, offsets, bad, W1.c, None, W2.c, None, Y, layer.ws)
+        assert torch.equal(Y[rest], clean[rest])
