@@ -99,6 +99,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, DeviceS
     }
 }
 
+// For a thread whose wait gave up: bulk copies and products that it has issued may still be on
+// their way and must be done before the block's shared and tensor memory go away.  They take
+// microseconds; what they would arrive on may never complete, so this waits a millisecond.
+__device__ __forceinline__ void settle() {
+    const uint64_t t0 = global_ns();
+    while (global_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
 // ---------------------------------------------------------------------------------------------
 // Async copies
 // ---------------------------------------------------------------------------------------------

@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            if (!ok) settle();
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (the pair's leader only) ----------------
@@ -538,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 if (PAIR) tc_commit_pair(tfull_bar(b)); else tc_commit(tfull_bar(b));
             }
+            if (!ok) settle();
         }
     } else if (warp < 2 + kEpiWarps) {
         // ---------------- epilogue (this CTA's 128 rows) ----------------

@@ -735,8 +735,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 else if constexpr (kTiles == 2)
                     w.template chunk<2>(stage + w_at, stage + s_at, stage + x_at, unpack, acc);
             }
+            // (A warp that gave up frees no stage: the copying warps then issue nothing over copies
+            // that have not landed, and find the last of them by the barriers' parity.)
             __syncwarp();
-            if (lane == 0) mbar_arrive(empty_bar(slot));
+            if (ok && lane == 0) mbar_arrive(empty_bar(slot));
             if (++slot == kStages) {
                 slot = 0;
                 phase ^= 1u;

@@ -52,3 +52,23 @@ def test_expert_ffn_w4_after_a_bad_index(moe, T):
         Y = torch.full_like(clean, 7.0)
         moe.moe_expert_ffn_packed(layer.p, x, offsets, bad, W1.c, None, W2.c, None, Y, layer.ws)
         assert torch.equal(Y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("T", [64, 1024])
+def test_expert_ffn_w4_under_a_timeout_and_after(moe, T):
+    """With a timeout in the status word a call ends (its waits may give up, its output is not used);
+    once the word is cleared, the next one gives the bits of the first."""
+    d, F, E, k = 2048, 1024, 64, 8
+    g = gen(62)
+    W1, W2 = make_experts(moe, g, E, F, F, d, (32, 128), True)
+    x = randn(g, T, d).to(torch.bfloat16)
+    offsets, rowtok = routing(g, T, E, k, "random")
+    layer = moe.MoELayer(T, d, F, E, k, w4=True)
+    clean = layer.expert_ffn_w4(x, offsets, rowtok, W1, None, W2, None)
+    moe.moe_selftest_wait_timeout(layer.ws, 1000)
+    for _ in range(3):
+        layer.expert_ffn_w4(x, offsets, rowtok, W1, None, W2, None)
+    assert status(moe, layer) == moe.DEV_TIMEOUT
+    moe.moe_reset_device_status(layer.ws)
+    assert torch.equal(layer.expert_ffn_w4(x, offsets, rowtok, W1, None, W2, None), clean)
+    assert status(moe, layer) == 0
