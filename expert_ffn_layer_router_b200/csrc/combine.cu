@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(256) ffn_f32_kernel(
     __syncthreads();
     const int e = s_e;
     const int t = rowtok[r];
-    if ((unsigned)t >= (unsigned)T) { if (threadIdx.x == 0) report(st, MOE_DEV_BAD_INDEX, 401); return; }
-    for (int i = threadIdx.x; i < d; i += blockDim.x) xs[i] = x[(size_t)t * d + i];
+    const bool known = (unsigned)t < (unsigned)T;       // else the row is computed from zeros
+    if (!known && threadIdx.x == 0) report(st, MOE_DEV_BAD_INDEX, 401);
+    for (int i = threadIdx.x; i < d; i += blockDim.x) xs[i] = known ? x[(size_t)t * d + i] : 0.0f;
     __syncthreads();
     const size_t F1 = gated ? 2 * (size_t)F : (size_t)F;    // W1 rows per expert
     const float* W1e = W1 + (size_t)e * F1 * d;

@@ -113,6 +113,11 @@ __device__ __forceinline__ void settle() {
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// 16 bytes to shared memory: copied (bytes = 16) or zeros (bytes = 0).
+__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
 // Arrives on `bar` (asynchronously) once every cp.async issued so far by this thread has
 // completed; the barrier's expected count includes this arrival (.noinc).
 __device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {

@@ -363,12 +363,6 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], const uint32_t (&a
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// 16 bytes to shared memory: copied (bytes = 16) or zeros (bytes = 0).
-__device__ __forceinline__ void cp_async_16z(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-
 __device__ __forceinline__ float silu(float v) { return v / (1.0f + __expf(-v)); }
 
 // A unit's place: expert, feature block, first row of the row tile, rows in it.

@@ -72,3 +72,36 @@ def test_expert_ffn_w4_under_a_timeout_and_after(moe, T):
     moe.moe_reset_device_status(layer.ws)
     assert torch.equal(layer.expert_ffn_w4(x, offsets, rowtok, W1, None, W2, None), clean)
     assert status(moe, layer) == 0
+
+
+@pytest.mark.parametrize("kind", ["w4", "bf16", "f32"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("T", [30, 700])
+def test_rows_of_a_bad_token_index_are_those_of_zeros(moe, kind, gated, T):
+    """A rowtok entry outside [0, T) gives the row that a token of zeros gives, bit for bit, whatever
+    the tiles held before; the other rows do not see it."""
+    d, F, E, k = 256, 128, 3, 2
+    g = gen(63)
+    layer = moe.MoELayer(T, d, F, E, k, dtype="f32" if kind == "f32" else "bf16",
+                         flags=moe.FLAG_GATED if gated else 0, w4=kind == "w4")
+    dt, F1 = layer.torch_dtype, 2 * F if gated else F
+    b1, b2 = randn(g, E, F1), randn(g, E, d)
+    if kind == "w4":
+        W1, W2 = make_experts(moe, g, E, F1, F, d, (64, 32), False)
+        ffn = layer.expert_ffn_w4
+    else:
+        W1, W2 = (randn(g, E, F1, d) / 16).to(dt), (randn(g, E, d, F) / 11).to(dt)
+        ffn = layer.expert_ffn
+    x = randn(g, T, d).to(dt)
+    x[T - 1] = 0
+    offsets, rowtok = routing(g, T, E, k, "random")
+    hit = torch.rand(T * k, generator=g, device=dev()) < 0.05
+    hit[[0, T, T * k - 1]] = True
+    zero = torch.where(hit, T - 1, rowtok)
+    want = ffn(x, offsets, zero, W1, b1, W2, b2)
+    ffn(torch.full_like(x, 3.0), offsets, rowtok, W1, b1, W2, b2)
+    assert status(moe, layer) == 0
+    for index in (T, -1, 2 ** 31 - 1, -2 ** 31):
+        got = ffn(x, offsets, torch.where(hit, index, rowtok), W1, b1, W2, b2)
+        assert torch.equal(got, want)
+        assert status(moe, layer) == moe.DEV_BAD_INDEX
