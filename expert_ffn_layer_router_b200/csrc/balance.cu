@@ -6,9 +6,11 @@
 //   losses[1] = sum_t lse_t^2 / n (router z-loss, lse_t = log sum_e exp L_te).
 // Gradient, with g = grad_losses and dw = the gradient of the k routing weights:
 //   dL_te = p_te (a_te - sum_c p_tc a_tc) + 2 g1 / n lse_t p_te,
-//   a_te  = g0 E f_e / n + sum_{j: ids[t,j] = e} dw'_tj,
-//   dw'_j = dw_j, or, for weights renormalised over the k, (dw_j - sum_i dw_i w_i) / S with
-//   S = sum_j p_j and w_j = p_j / S.
+//   a_te  = g0 E f_e / n + sum_{j: ids[t,j] = e} dw_tj.
+// Weights renormalised over the k are a softmax of their own, w = softmax(L_tj over j): their part of
+// dL_te is sum_{j: ids[t,j] = e} w_j (dw_j - sum_i dw_i w_i), added as it is.  (Through p it would be
+// p_te (..) / sum_j p_j, which is 0 / 0 or overflows where the named experts lie some 90 below the
+// row's maximum.  Its sum over a row is 0, so it has no share in the other sum.)
 //
 // Layout.  A group of G lanes holds one token's logits in registers, 4 NV per lane (16-byte loads
 // when rows allow), so a row is read once and every sum over the experts is log2 G shuffles.
@@ -347,14 +349,16 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
         const int e = expert_of<G, VEC>(l, i);
         base[i] = grad_losses && e < E ? scale * (float)counts[e] : 0.0f;
     }
-    // grad_w: the group's row of dw' (zeros between tokens) and of the lanes that own its entries.
-    extern __shared__ float s_rows[];
+    // grad_w: the group's row of dw (zeros between tokens) and of the lanes that own its entries.
+    // Renormalised: of the finished terms of dL instead.
+    extern __shared__ __align__(16) float s_rows[];
     float* row = s_rows + (threadIdx.x / G) * E;
     uint8_t* own = reinterpret_cast<uint8_t*>(s_rows + kGroups * E) + (threadIdx.x / G) * E;
     if (grad_w) {
         for (int e = l; e < E; e += G) row[e] = 0.0f;
         __syncwarp();
     }
+    const bool added = renorm && grad_w;
     const long long all = (long long)gridDim.x * kGroups;
     const long long steps = (T + all - 1) / all;
     long long t = (long long)blockIdx.x * kGroups + threadIdx.x / G;
@@ -388,20 +392,24 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
 #pragma unroll
         for (int q = 0; q < 4 * NV; ++q) a[q] = base[q];
         if (grad_w) {
-            // Lane j < k of the group holds pair j: its expert and dw'.
+            // Lane j < k of the group holds pair j: its expert and dw.
             if (live && l < k && (id < 0 || id >= E)) {
                 report(st, MOE_DEV_BAD_INDEX, 620);
                 id = -1;
                 dw = 0.0f;
             }
             if (renorm) {
-                const float pj = id >= 0 ? exp_of(logits[at * E + id] - ms.x) * r : 0.0f;
-                const float S = group_sum<G>(pj);
-                const float d = group_sum<G>(dw * pj);
-                dw = S > 0.0f ? (dw - d / S) / S : 0.0f;
+                const float kNone = __int_as_float(0xff800000);
+                const float lj = id >= 0 ? logits[at * E + id] : kNone;
+                const float top = group_max<G>(lj);
+                const float u = lj > kNone ? exp_of(lj - top) : 0.0f;
+                const float sum = group_sum<G>(u);             // (at least 1, or no pair: 0)
+                const float d = group_sum<G>(dw * u);
+                const float rs = __frcp_rn(sum > 0.0f ? sum : 1.0f);
+                dw = u * rs * (dw - d * rs);
             }
             // An expert named twice: the lane that did not win its entry sees another's number
-            // there, and its pairs' dw' are added up (in pair order) in every lane that names it.
+            // there, and its pairs' dw are added up (in pair order) in every lane that names it.
             if (id >= 0) own[id] = (uint8_t)l;
             __syncwarp();
             if (__any_sync(kFull, id >= 0 && own[id] != l)) {
@@ -415,13 +423,13 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
             }
             if (id >= 0) row[id] = dw;
             __syncwarp();
+            if (!renorm) {
 #pragma unroll
-            for (int q = 0; q < 4 * NV; ++q) {
-                const int e = expert_of<G, VEC>(l, q);
-                if (e < E) a[q] += row[e];
+                for (int q = 0; q < 4 * NV; ++q) {
+                    const int e = expert_of<G, VEC>(l, q);
+                    if (e < E) a[q] += row[e];
+                }
             }
-            __syncwarp();
-            if (id >= 0) row[id] = 0.0f;
         }
         float dot = 0.0f;
 #pragma unroll
@@ -437,19 +445,27 @@ __global__ void __launch_bounds__(kThreadsOf<NV>)
 #pragma unroll
                 for (int q = 0; q < NV; ++q) {
                     const int e = 4 * (l + G * q);
-                    if (e < E)
-                        *reinterpret_cast<float4*>(out + e) = make_float4(
-                            v[4 * q] * (a[4 * q] + shift), v[4 * q + 1] * (a[4 * q + 1] + shift),
-                            v[4 * q + 2] * (a[4 * q + 2] + shift),
-                            v[4 * q + 3] * (a[4 * q + 3] + shift));
+                    if (e < E) {
+                        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (added) x = *reinterpret_cast<const float4*>(row + e);
+                        *reinterpret_cast<float4*>(out + e) =
+                            make_float4(fmaf(v[4 * q], a[4 * q] + shift, x.x),
+                                        fmaf(v[4 * q + 1], a[4 * q + 1] + shift, x.y),
+                                        fmaf(v[4 * q + 2], a[4 * q + 2] + shift, x.z),
+                                        fmaf(v[4 * q + 3], a[4 * q + 3] + shift, x.w));
+                    }
                 }
             } else {
 #pragma unroll
                 for (int q = 0; q < 4 * NV; ++q) {
                     const int e = l + G * q;
-                    if (e < E) out[e] = v[q] * (a[q] + shift);
+                    if (e < E) out[e] = fmaf(v[q], a[q] + shift, added ? row[e] : 0.0f);
                 }
             }
+        }
+        if (grad_w) {
+            __syncwarp();
+            if (id >= 0) row[id] = 0.0f;
         }
     }
 }

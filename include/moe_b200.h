@@ -309,8 +309,9 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
  * float32 on the device, with counts as moe_balance_loss gives them, or summed over the ranks of
  * a group; NULL leaves this part out), plus that of the k routing weights w_tj, given their
  * gradient grad_w [T k] float32 (NULL leaves it out; ids is read only with it, and is held
- * constant).  MOE_FLAG_RENORMALIZE: the weights are the renormalised ones.  At least one of the
- * two is given.  An id outside [0, E) is left out and recorded as MOE_DEV_BAD_INDEX; an id named
+ * constant).  MOE_FLAG_RENORMALIZE: the weights are the renormalised ones, a softmax over the k
+ * named logits wherever these lie in the row (named experts of -infinity have weight 0; where all
+ * are, this part is 0).  At least one of the two is given.  An id outside [0, E) is left out and recorded as MOE_DEV_BAD_INDEX; an id named
  * twice by a token adds up.  dlogits must not alias logits. */
 moe_status moe_route_backward(const moe_problem* p, const float* logits, const int32_t* ids,
                               const uint8_t* mask, const int32_t* counts,

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 from tests.gpu_util import dev
-from tests.test_gpu_operators import gen, make_experts, moe, randn, routing, status  # noqa: F401
+from tests.test_gpu_operators import (U, assert_within, gen, make_experts, moe, randn,  # noqa: F401
+                                      routing, status)
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,62 @@ def test_rows_of_a_bad_token_index_are_those_of_zeros(moe, kind, gated, T):
         got = ffn(x, offsets, torch.where(hit, index, rowtok), W1, b1, W2, b2)
         assert torch.equal(got, want)
         assert status(moe, layer) == moe.DEV_BAD_INDEX
+
+
+def renormalised_reference(logits, ids, grad_w):
+    """The renormalised weights' part of dlogits in 64 bits, from w = softmax over the named logits,
+    and the magnitude of its terms.  Ids outside [0, E) are left out."""
+    T, E = logits.shape
+    I = ids.long()
+    ok = (I >= 0) & (I < E)
+    L = torch.gather(logits.double(), 1, I.clamp(0, E - 1)).masked_fill(~ok, -math.inf)
+    top = L.amax(1, keepdim=True)
+    u = torch.where(L > -math.inf, torch.exp(L - torch.where(top > -math.inf, top, 0.0)), 0.0)
+    w = u / u.sum(1, keepdim=True).clamp(min=1e-300)
+    dw = grad_w.double() * ok
+    term = w * (dw - (w * dw).sum(1, keepdim=True))
+    mag = w * (dw.abs() + (w * dw.abs()).sum(1, keepdim=True))
+    out, terms = (torch.zeros(T, E, dtype=torch.float64, device=dev()) for _ in range(2))
+    out.scatter_add_(1, I.clamp(0, E - 1), term * ok)
+    terms.scatter_add_(1, I.clamp(0, E - 1), mag * ok)
+    return out, terms
+
+
+@pytest.mark.parametrize("gap", [0, 60, 85, 95, 100, 120, 1000, 1e30])
+@pytest.mark.parametrize("E,k", [(8, 2), (30, 5), (64, 6), (128, 8), (400, 32)])
+def test_renormalised_gradient_far_below_the_maximum(moe, gap, E, k):
+    """Named experts `gap` below the row's maximum: their weights are a softmax of their own, with
+    finite gradients.  w's relative error: the rounding of L - top (|L - top| < 20 here; at 1e30 the
+    logits are equal), exp within 2 ulp (4 U), sums of k terms, reciprocal and products: at most 2 (20
+    + 4 + k + 4) U in each of the two terms."""
+    T = 41
+    g = gen(E + k)
+    logits = 2 * randn(g, T, E)
+    ids = torch.argsort(torch.rand(T, E, generator=g, device=dev()), 1)[:, :k].contiguous().to(torch.int32)
+    named = torch.zeros(T, E, dtype=torch.bool, device=dev()).scatter_(1, ids.long(), True)
+    named[5] = False                                        # (a row that names its maximum too)
+    logits = torch.where(named, logits - gap, logits).float()
+    ids[7, 0] = E                                           # left out
+    ids[9, 1] = ids[9, 0]                                   # named twice
+    logits[11, ids[11, 0].long()] = -math.inf               # weight 0
+    logits[12, ids[12].long()] = -math.inf                  # no weights at all
+    if gap == 1e30:
+        logits[11] = -1e30                                  # (with the row's maximum a named one too)
+        logits[11, ids[11, 0].long()] = -math.inf
+    grad_w = randn(g, T, k)
+    layer = moe.MoELayer(T, 64, 64, E, k, flags=moe.FLAG_RENORMALIZE)
+    got = layer.route_backward(logits, ids, grad_w=grad_w)
+    assert status(moe, layer) == moe.DEV_BAD_INDEX
+    want, terms = renormalised_reference(logits, ids, grad_w)
+    assert_within(got, want, 4 * (20 + 8 + k) * U * terms + 1e-37, "dlogits")
+    assert (got[12] == 0).all() and (got[~named & (torch.arange(T, device=dev()) != 5)[:, None]] == 0).all()
+    # The losses' gradient is added to it.
+    gl = torch.tensor([0.7, -0.3], device=dev())
+    live = logits.clone()
+    live[12] = 0                                            # (a row needs one finite logit)
+    _, counts, _ = layer.balance_loss(live, ids)
+    alone = layer.route_backward(live, ids, counts, gl)
+    both = layer.route_backward(live, ids, counts, gl, grad_w)
+    want, terms = renormalised_reference(live, ids, grad_w)
+    assert_within(both, alone.double() + want, 4 * (20 + 8 + k) * U * terms + 2 * U * alone.abs().double() +
+                  1e-37, "dlogits with the losses")
