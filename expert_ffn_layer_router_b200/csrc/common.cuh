@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <mutex>
 
 #include "../../include/moe_b200.h"
 
@@ -252,16 +253,21 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 }
 
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device (raised as needed; a
-// kernel's limit is asked for once per device, as the driver call costs a microsecond).
+// kernel's limit is asked for once per device, as the driver call costs a microsecond).  Raised by
+// one thread at a time: a smaller size set after a larger one would lower the limit again.
+inline std::mutex g_smem_mutex;
 template <typename... KArgs>
 cudaError_t allow_smem(void (*kernel)(KArgs...), std::atomic<int> (&allowed)[64], int bytes) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return note_launch(e);
-    if (dev < 64 && allowed[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    auto enough = [&] { return dev < 64 && allowed[dev].load(std::memory_order_acquire) >= bytes; };
+    if (enough()) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(g_smem_mutex);
+    if (enough()) return cudaSuccess;
     e = note_launch(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          bytes));
-    if (e == cudaSuccess && dev < 64) allowed[dev].store(bytes, std::memory_order_relaxed);
+    if (e == cudaSuccess && dev < 64) allowed[dev].store(bytes, std::memory_order_release);
     return e;
 }
 

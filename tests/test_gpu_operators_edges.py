@@ -165,3 +165,44 @@ def test_renormalised_gradient_far_below_the_maximum(moe, gap, E, k):
     want, terms = renormalised_reference(live, ids, grad_w)
     assert_within(both, alone.double() + want, 4 * (20 + 8 + k) * U * terms + 2 * U * alone.abs().double() +
                   1e-37, "dlogits with the losses")
+
+
+def test_layers_on_threads(moe):
+    """Layers of different numbers of experts (and so of different shared-memory sizes), each on a
+    thread and a stream of its own at once, give the bits that they give alone."""
+    import threading
+    T, d, F, k = 48, 128, 128, 2
+    jobs = []
+    for n, E in enumerate((1024, 3, 700, 40, 1000, 8)):
+        g = gen(70 + n)
+        layer = moe.MoELayer(T, d, F, E, k, flags=moe.FLAG_GATED if n % 2 else 0, w4=True)
+        W1, W2 = make_experts(moe, g, E, 2 * F if n % 2 else F, F, d, ((32, 64, 128)[n % 3], 32), n < 3)
+        x, logits = randn(g, T, d).to(torch.bfloat16), randn(g, T, E)
+        ids = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+        jobs.append((layer, x, routing(g, T, E, k, "random"), W1, W2, logits, ids, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(job):
+        layer, x, route, W1, W2, logits, ids, stream = job
+        return [(layer.expert_ffn_w4(x, *route, W1, None, W2, None, stream=stream),
+                 *layer.balance_loss(logits, ids, stream=stream)) for _ in range(20)]
+
+    got, start = [None] * len(jobs), threading.Barrier(len(jobs))
+
+    def run(n):
+        start.wait()
+        got[n] = work(jobs[n])
+
+    threads = [threading.Thread(target=run, args=(n,)) for n in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for job, results in zip(jobs, got):
+        want = work(job)[0]
+        torch.cuda.synchronize()
+        for r in results:
+            for a, b in zip(r, want):
+                assert torch.equal(a, b)
+        assert status(moe, job[0]) == 0
