@@ -50,6 +50,19 @@ __device__ __forceinline__ uint16_t bf16_round(float v) {
 // (64 x 1024 x 2048 from bfloat16, 0.34 GB moved: 90 us, 52 at the copy bandwidth; issue-bound.  With a
 // division near halves 143 us, half of the warps meeting one.)
 // ------------------------------------------------------------------------------------------------
+// A NaN reaches its group's extremes (and so the scale), and an infinity makes the scale infinite; both
+// take the dividing path, whose nibbles stay in their places.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 constexpr float kRound = 12582920.0f;                  // 1.5 * 2^23 + 8 (even: halves stay halves)
 constexpr uint32_t kRoundBits = 0x4b400008u - 8u;      // its bits, without the 8
 
@@ -123,24 +136,24 @@ __global__ void __launch_bounds__(256)
                 float lo = in ? v[0] : kInf, hi = in ? v[0] : -kInf;
 #pragma unroll
                 for (int i = 1; i < 8; ++i) {
-                    lo = fminf(lo, in ? v[i] : kInf);
-                    hi = fmaxf(hi, in ? v[i] : -kInf);
+                    lo = min_nan(lo, in ? v[i] : kInf);
+                    hi = max_nan(hi, in ? v[i] : -kInf);
                 }
 #pragma unroll
                 for (int h = 1; h < kLanes; h *= 2) {
-                    lo = fminf(lo, __shfl_xor_sync(kFull, lo, h));
-                    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, h));
+                    lo = min_nan(lo, __shfl_xor_sync(kFull, lo, h));
+                    hi = max_nan(hi, __shfl_xor_sync(kFull, hi, h));
                 }
-                const bool any = hi >= lo;
+                const bool any = !(hi < lo);
                 s = any ? bf16_bits(bf16_round(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f))) : 0.0f;
                 z = any ? bf16_bits(bf16_round(__fadd_rn(lo, __fmul_rn(8.0f, s)))) : 0.0f;
             } else {
                 float top = fabsf(v[0]);
 #pragma unroll
-                for (int i = 1; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+                for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(v[i]));
 #pragma unroll
                 for (int h = 1; h < kLanes; h *= 2)
-                    top = fmaxf(top, __shfl_xor_sync(kFull, top, h));
+                    top = max_nan(top, __shfl_xor_sync(kFull, top, h));
                 s = bf16_bits(bf16_round(__fmul_rn(top, 1.0f / 7.0f)));
             }
             const float inv = __frcp_rn(s);
@@ -155,7 +168,7 @@ __global__ void __launch_bounds__(256)
             }
             uint32_t word = acc - kRoundBits * 0x11111111u;
             // (without offsets |t| stays below 7.1 for such s, so nothing has to be clamped)
-            if (!(s > 7.9e-31f)) {
+            if (!(s > 7.9e-31f && s < kInf)) {
                 word = 0;
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {

@@ -397,8 +397,8 @@ class W4Weights:
 
 
 def quantize_w4(W, group, zeros=False, stream=None) -> W4Weights:
-    """Quantises ``W`` [E, N, K] (bfloat16 or float32, finite) to 4 bits with a scale, and with
-    ``zeros`` an offset, per ``group`` columns."""
+    """Quantises ``W`` [E, N, K] (bfloat16 or float32) to 4 bits with a scale, and with ``zeros`` an
+    offset, per ``group`` columns.  A group with a NaN or an infinity reads back as not finite."""
     if not isinstance(W, torch.Tensor) or W.dim() != 3 or W.dtype not in (torch.bfloat16,
                                                                          torch.float32):
         raise MoeError(MOE_ERR_INVALID_ARG, "quantize_w4: W must be bfloat16 or float32 [E, N, K]")

@@ -238,8 +238,9 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
                        size_t ws_bytes, void* stream);
 
 /* ---- 4-bit expert weights ------------------------------------------------------------------
- * Quantises W [E, N, K] (dtype MOE_BF16 or MOE_F32, dense, 16-byte aligned; values finite, below
- * 2^126 in magnitude) to the format of moe_w4.  Per group, zero = NULL: scale = max|w| / 7; else
+ * Quantises W [E, N, K] (dtype MOE_BF16 or MOE_F32, dense, 16-byte aligned; values below 2^126 in
+ * magnitude) to the format of moe_w4.  A group that holds a NaN or an infinity gets a scale that is
+ * not finite and reads back as values that are not finite; the other groups do not see it.  Per group, zero = NULL: scale = max|w| / 7; else
  * scale = (max - min) / 15 and zero = min + 8 scale.  Both are rounded to bfloat16 first (the
  * differences, products with the float32 reciprocal of 7 or 15, and sums in float32), then
  * nibble - 8 = round-half-even((w - zero) / scale), clamped to [-8, 7]; 0 where scale = 0.

@@ -206,3 +206,34 @@ def test_layers_on_threads(moe):
             for a, b in zip(r, want):
                 assert torch.equal(a, b)
         assert status(moe, job[0]) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_quantize_keeps_what_is_not_finite_in_its_group(moe, dtype, zeros, group, value):
+    """A NaN or an infinity makes its own group's values not finite and changes no other group."""
+    E, N, K = 2, 35, 576
+    g = gen(80)
+    W = randn(g, E, N, K).to(dtype)
+    clean = moe.quantize_w4(W, group, zeros=zeros)
+    hit = torch.rand(E, N, K, generator=g, device=dev()) < 0.002
+    hit[1, 34, 575] = hit[0, 0, 0] = True
+    w = moe.quantize_w4(torch.where(hit, torch.full_like(W, value), W), group, zeros=zeros)
+    G = -(-K // group)
+    in_group = torch.nn.functional.pad(hit, (0, G * group - K)).view(E, N, G, group).any(3)
+    keep = ~in_group.transpose(1, 2)
+    assert keep.any() and not keep.all()
+    assert torch.equal(w.scale[keep], clean.scale[keep])
+    assert not torch.isfinite(w.scale[~keep]).any()
+    if zeros:
+        assert torch.equal(w.zero[keep], clean.zero[keep])
+    cols = in_group.repeat_interleave(group, 2)[:, :, :K]
+    back, want = moe.dequantize_w4(w), moe.dequantize_w4(clean)
+    assert torch.equal(back[~cols], want[~cols])
+    assert not torch.isfinite(back[cols]).any()
+    # The words past K, whose nibbles are 8, hold the same bits.
+    past = torch.arange(16 * (-(-K // 128)), device=dev())
+    first = 128 * (past // 16) + 32 * (past % 4) + 8 * (past % 16 // 4)
+    assert (w.q[:, :, first >= K] == -0x77777778).all()
