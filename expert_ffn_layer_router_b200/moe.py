@@ -371,27 +371,50 @@ class _on:
 class W4Weights:
     """4-bit weights [E, N, K] with group scales: ``q`` [E, N, 16 ceil(K/128)] int32 words,
     ``scale`` and the optional offsets ``zero`` [E, ceil(K/group), N] bfloat16 (the layout of
-    moe_w4).  :func:`quantize_w4` makes them."""
+    moe_w4).  :func:`quantize_w4` makes them.  The tensors' values may change in place; other
+    tensors take another object."""
+
+    __slots__ = ("_tensors", "_shapes", "_sizes", "_device")
+    q = property(lambda self: self._tensors[0])
+    scale = property(lambda self: self._tensors[1])
+    zero = property(lambda self: self._tensors[2])
+    E = property(lambda self: self._sizes[0])
+    N = property(lambda self: self._sizes[1])
+    K = property(lambda self: self._sizes[2])
+    group = property(lambda self: self._sizes[3])
 
     def __init__(self, q, scale, zero=None, *, K, group):
-        E, N = q.shape[:2]
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise MoeError(MOE_ERR_INVALID_ARG, "W4Weights: q must be int32 words [E, N, ...]")
         if group not in (32, 64, 128):
             raise MoeError(MOE_ERR_INVALID_ARG, "W4Weights: group must be 32, 64 or 128")
-        dev, side = q.device, (E, -(-K // group), N)
-        _need("W4Weights", "q", q, torch.int32, (E, N, 16 * (-(-K // 128))), dev)
-        _need("W4Weights", "scale", scale, torch.bfloat16, side, dev)
+        E, N, dev = q.shape[0], q.shape[1], q.device
+        shapes = ((E, N, 16 * (-(-K // 128))), (E, -(-K // group), N))
+        _need("W4Weights", "q", q, torch.int32, shapes[0], dev)
+        _need("W4Weights", "scale", scale, torch.bfloat16, shapes[1], dev)
         if zero is not None:
-            _need("W4Weights", "zero", zero, torch.bfloat16, side, dev)
-        self._set(q, scale, zero, E, N, K, group)
+            _need("W4Weights", "zero", zero, torch.bfloat16, shapes[1], dev)
+        self._tensors, self._shapes = (q, scale, zero), shapes
+        self._sizes, self._device = (E, N, int(K), int(group)), dev
 
-    def _set(self, q, scale, zero, E, N, K, group):
-        self.q, self.scale, self.zero = q, scale, zero
-        self.E, self.N, self.K, self.group = E, N, int(K), int(group)
-        self.c = W4(q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
-                    self.group)
+    @property
+    def c(self):
+        """The tensors' present addresses as a moe_w4.  (A tensor can be given other storage or
+        another shape in place, so each call looks at them.)"""
+        q, scale, zero = self._tensors
+        words, side = self._shapes
+        if (q.shape != words or scale.shape != side or not q.is_contiguous() or
+                not scale.is_contiguous() or q.device != self._device or
+                scale.device != self._device or (zero is not None and (
+                    zero.shape != side or not zero.is_contiguous() or
+                    zero.device != self._device))):
+            raise MoeError(MOE_ERR_INVALID_ARG, "W4Weights: a tensor was changed to another shape, "
+                           "layout or device")
+        return W4(q.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr(),
+                  self._sizes[3])
 
     def _need(self, what, name, shape, device):
-        if (self.E, self.N, self.K) != tuple(shape) or self.q.device != device:
+        if self._sizes[:3] != tuple(shape) or self._device != device:
             raise MoeError(MOE_ERR_INVALID_ARG, "%s: %s must be 4-bit weights of shape %s on %s"
                            % (what, name, tuple(shape), device))
 
@@ -412,9 +435,7 @@ def quantize_w4(W, group, zeros=False, stream=None) -> W4Weights:
         scale = torch.empty(side, dtype=torch.bfloat16, device=W.device)
         zero = torch.empty(side, dtype=torch.bfloat16, device=W.device) if zeros else None
         moe_quantize_packed(W, E, N, K, group, q, scale, zero, st)
-    w = W4Weights.__new__(W4Weights)
-    w._set(q, scale, zero, E, N, K, group)
-    return w
+    return W4Weights(q, scale, zero, K=K, group=group)
 
 
 def dequantize_w4(w: W4Weights, stream=None):

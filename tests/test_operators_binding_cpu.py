@@ -1,0 +1,50 @@
+"""The binding's side of the calls around the layer, on host tensors (no GPU needed): what it keeps
+between calls, and what it refuses."""
+import pytest
+import torch
+
+from expert_ffn_layer_router_b200 import build as lib_build
+
+
+@pytest.fixture(scope="module")
+def moe():
+    lib_build.build()
+    from expert_ffn_layer_router_b200 import moe as m
+    return m
+
+
+def packed(moe, E=4, N=64, K=192, group=64, zeros=True):
+    side = (E, -(-K // group), N)
+    return moe.W4Weights(torch.zeros(E, N, 16 * (-(-K // 128)), dtype=torch.int32),
+                         torch.zeros(side, dtype=torch.bfloat16),
+                         torch.zeros(side, dtype=torch.bfloat16) if zeros else None, K=K, group=group)
+
+
+@pytest.mark.parametrize("name", ["q", "scale", "zero"])
+def test_packed_weights_follow_their_tensors(moe, name):
+    """The addresses a call gets are those of the tensors at the call: a tensor cannot be replaced
+    behind them, and one that was given other storage in place is followed or refused."""
+    w = packed(moe)
+    t = getattr(w, name)
+    assert (w.c.q, w.c.scale, w.c.zero, w.c.group) == (w.q.data_ptr(), w.scale.data_ptr(),
+                                                       w.zero.data_ptr(), 64)
+    with pytest.raises(AttributeError):
+        setattr(w, name, t.clone())
+    moved = t.clone()
+    t.set_(moved)
+    assert getattr(w.c, name) == moved.data_ptr()
+    t.resize_(1)
+    with pytest.raises(moe.MoeError):
+        w.c
+    assert packed(moe, zeros=False).c.zero is None
+
+
+def test_packed_weights_are_checked(moe):
+    q, s = torch.zeros(2, 32, 16, dtype=torch.int32), torch.zeros(2, 2, 32, dtype=torch.bfloat16)
+    ok = moe.W4Weights(q, s, K=128, group=64)
+    assert (ok.E, ok.N, ok.K, ok.group) == (2, 32, 128, 64)
+    for args, kw in (((None, s), {}), ((q[0], s), {}), ((q, None), {}), ((q, s.float()), {}),
+                     ((q, s, s[:1]), {}), ((q.long(), s), {}), ((q, s), dict(group=32)),
+                     ((q, s), dict(K=64)), ((q, s), dict(K=256)), ((q.transpose(0, 1), s), {})):
+        with pytest.raises(moe.MoeError):
+            moe.W4Weights(*args, **{**dict(K=128, group=64), **kw})
