@@ -7,8 +7,10 @@ There is no CPU path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
+import operator
 import os
 
 import torch
@@ -343,7 +345,7 @@ class _on:
     __slots__ = ("device", "stream", "guards")
 
     def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
+        self.device, self.stream, self.guards = device, stream, None
 
     def __enter__(self):
         index = self.device.index
@@ -351,20 +353,29 @@ class _on:
             raise MoeError(MOE_ERR_INVALID_ARG, "tensors must be on a CUDA device, not on %s" % self.device)
         if self.stream is None and index == torch._C._cuda_getDevice():
             return torch._C._cuda_getCurrentRawStream(index)
-        guards = [torch.cuda.device(self.device)]
-        guards[0].__enter__()
-        if self.stream is not None:
-            st = self.stream
-            if not hasattr(st, "cuda_stream"):
-                st = torch.cuda.ExternalStream(int(st), device=self.device)
-            guards.append(torch.cuda.stream(st))
-            guards[1].__enter__()
-        self.guards = guards
+        with contextlib.ExitStack() as guards:             # (undone if the stream cannot be used)
+            guards.enter_context(torch.cuda.device(self.device))
+            if self.stream is not None:
+                guards.enter_context(torch.cuda.stream(self._stream()))
+            self.guards = guards.pop_all()
         return torch._C._cuda_getCurrentRawStream(index)
 
+    def _stream(self):
+        st = self.stream
+        if hasattr(st, "cuda_stream"):
+            if st.device != self.device:
+                raise MoeError(MOE_ERR_INVALID_ARG, "stream is on %s, the tensors on %s"
+                               % (st.device, self.device))
+            return st
+        try:
+            handle = operator.index(st)
+        except TypeError:
+            raise MoeError(MOE_ERR_INVALID_ARG, "stream must be a CUDA stream or its handle") from None
+        return torch.cuda.ExternalStream(handle, device=self.device)
+
     def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+        if self.guards is not None:
+            self.guards.__exit__(*exc)
         return False
 
 

@@ -48,3 +48,42 @@ def test_packed_weights_are_checked(moe):
                      ((q, s), dict(K=64)), ((q, s), dict(K=256)), ((q.transpose(0, 1), s), {})):
         with pytest.raises(moe.MoeError):
             moe.W4Weights(*args, **{**dict(K=128, group=64), **kw})
+
+
+class FakeGuard:
+    depth = 0
+
+    def __init__(self, *a):
+        pass
+
+    def __enter__(self):
+        FakeGuard.depth += 1
+
+    def __exit__(self, *exc):
+        FakeGuard.depth -= 1
+        return False
+
+
+class FakeStream:
+    cuda_stream = 1 << 20
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+def test_streams_that_cannot_be_used(moe, monkeypatch):
+    """A stream of another device than the tensors', or something that is no stream, is refused (the
+    work would have run on another stream than the caller ordered), and the current device and stream
+    are what they were."""
+    monkeypatch.setattr(torch.cuda, "device", FakeGuard)
+    monkeypatch.setattr(torch.cuda, "stream", FakeGuard)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 77, raising=False)
+    dev = torch.device("cuda", 0)
+    for stream in (FakeStream(1), "stream", 1.5, object()):
+        with pytest.raises(moe.MoeError):
+            with moe._on(dev, stream):
+                pass
+        assert FakeGuard.depth == 0
+    with moe._on(dev, FakeStream(0)) as handle:
+        assert handle == 77 and FakeGuard.depth == 2
+    assert FakeGuard.depth == 0
