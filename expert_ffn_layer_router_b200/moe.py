@@ -230,7 +230,7 @@ def moe_workspace_size_packed(p: Problem) -> int:
 
 
 def moe_quantize_packed(W, E, N, K, group, q, scale, zero=None, stream=None):
-    dtype = MOE_BF16 if W.dtype == torch.bfloat16 else MOE_F32
+    dtype = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}.get(W.dtype, -1)     # (-1: refused)
     _check(_lib.moe_quantize_packed(_at(W), dtype, int(E), int(N), int(K), int(group), _at(q),
                                 _at(scale), _at(zero), _at_stream(stream)), "moe_quantize_packed")
 
@@ -451,6 +451,8 @@ def quantize_w4(W, group, zeros=False, stream=None) -> W4Weights:
 
 def dequantize_w4(w: W4Weights, stream=None):
     """The values of 4-bit weights, bfloat16 [E, N, K]."""
+    if not isinstance(w, W4Weights):
+        raise MoeError(MOE_ERR_INVALID_ARG, "dequantize_w4: w must be W4Weights")
     with _on(w.q.device, stream) as st:
         W = torch.empty((w.E, w.N, w.K), dtype=torch.bfloat16, device=w.q.device)
         moe_dequantize_packed(w.c, w.E, w.N, w.K, W, st)
@@ -665,7 +667,7 @@ class MoELayer:
             raise MoeError(MOE_ERR_INVALID_ARG, what + ": W1 and W2 must be W4Weights")
         _need(what, "x", x, torch.bfloat16, (p.T, p.d_model), dev)
         _need(what, "offsets", offsets, torch.int32, (p.E + 1,), dev)
-        rows = rowtok.numel()
+        rows = rowtok.numel() if isinstance(rowtok, torch.Tensor) else 0
         _need(what, "rowtok", rowtok, torch.int32, (max(self.max_rows, rows),), dev)
         self._need_experts(what, W1, b1, W2, b2)
         with _on(dev, stream) as st:
@@ -691,6 +693,8 @@ class MoELayer:
             _need(what, "br", br, torch.float32, (p.E,), dev)
         self._need_experts(what, W1, b1, W2, b2)
         if norm is not None:
+            if not isinstance(norm, (tuple, list)) or len(norm) != 3:
+                raise MoeError(MOE_ERR_INVALID_ARG, what + ": norm must be (gamma, beta, eps)")
             for name, t in (("gamma", norm[0]), ("beta", norm[1])):
                 _need(what, name, t, torch.float32, (p.d_model,), dev)
         with _on(dev, stream) as st:

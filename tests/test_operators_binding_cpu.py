@@ -87,3 +87,26 @@ def test_streams_that_cannot_be_used(moe, monkeypatch):
     with moe._on(dev, FakeStream(0)) as handle:
         assert handle == 77 and FakeGuard.depth == 2
     assert FakeGuard.depth == 0
+
+
+def test_arguments_of_another_kind(moe):
+    """What is no tensor, no 4-bit weight or of a type that a call does not take raises the library's
+    error before anything is read (half-precision weights would have been read as float32)."""
+    half = torch.zeros(1, 32, 64, dtype=torch.float16)
+    q, s = torch.zeros(1, 32, 16, dtype=torch.int32), torch.zeros(1, 2, 32, dtype=torch.bfloat16)
+    layer = moe.MoELayer(16, 64, 64, 4, 2, device="cpu", w4=True)
+    x, f = torch.zeros(16, 64, dtype=torch.bfloat16), torch.zeros(64)
+    w, counts = packed(moe, N=64, K=64), torch.zeros(5, dtype=torch.int32)
+    calls = [lambda: moe.moe_quantize_packed(half, 1, 32, 64, 32, q, s, None, 0),
+             lambda: moe.moe_quantize_packed(half.double(), 1, 32, 64, 32, q, s, None, 0),
+             lambda: moe.quantize_w4(half, 32), lambda: moe.quantize_w4(None, 32),
+             lambda: moe.dequantize_w4(q), lambda: moe.dequantize_w4(None)]
+    calls += [lambda r=r: layer.expert_ffn_w4(x, counts, r, w, None, w, None)
+              for r in (None, [0] * 32, torch.zeros(32))]
+    calls += [lambda n=n: layer.forward_block(x, torch.zeros(64, 4), None, w, None, w, None, norm=n)
+              for n in (f, (f, f), (f, None, 1e-5), (None, f, 1e-5))]
+    for n, call in enumerate(calls):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.status == moe.MOE_ERR_INVALID_ARG, n
+        assert "CUDA device" not in str(e.value), n
