@@ -239,10 +239,13 @@ size_t w4_copy_bytes(const moe_problem* p) {
 moe_status ffn_w4_steps(const moe_problem* p, const void* x, const int32_t* offsets,
                         const int32_t* rowtok, const moe_w4* W1, const float* b1,
                         const moe_w4* W2, const float* b2, void* Y, void* ws, const Plan& q,
-                        cudaStream_t s, int* launches) {
+                        cudaStream_t s, int* launches, bool stages = false) {
     moe::DeviceStatus* st = at<moe::DeviceStatus>(ws, q.status);
     const long long R = max_rows_of(p, capacity_of(p));
-    if (R == 0) return MOE_OK;
+    if (R == 0) {
+        if (stages) stage_mark(4, s);
+        return MOE_OK;
+    }
     const int g1 = (p->flags & MOE_FLAG_GATED) ? 2 : 0, N1 = w4_rows1(p);
     const int d = p->d_model, F = p->d_ff, E = p->E;
     void* H = at<void>(ws, q.H);
@@ -254,6 +257,7 @@ moe_status ffn_w4_steps(const moe_problem* p, const void* x, const int32_t* offs
         e = moe::launch_w4_gemm(g1, x, rowtok, p->T, offsets, E, d, N1, (int)R, q1(W1), sc(W1),
                                 ze(W1), W1->group, b1, H, F, st, s, launches);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
+        if (stages) stage_mark(4, s);
         e = moe::launch_w4_gemm(1, H, nullptr, (int)R, offsets, E, F, d, (int)R, q1(W2), sc(W2),
                                 ze(W2), W2->group, b2, Y, d, st, s, launches);
         return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -263,6 +267,7 @@ moe_status ffn_w4_steps(const moe_problem* p, const void* x, const int32_t* offs
     e = moe::launch_expert_gemm(g1, x, d, rowtok, p->T, offsets, E, d, F, W, b1, H, F, R, st, s,
                                 launches);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (stages) stage_mark(4, s);
     moe::launch_w4_dequantize(q1(W2), sc(W2), ze(W2), E, d, F, W2->group, W, s, launches);
     e = moe::launch_expert_gemm(1, H, F, nullptr, (int)R, offsets, E, F, d, W, b2, Y, d, R, st, s,
                                 launches);
@@ -365,7 +370,8 @@ void* static_scratch_for_current_context(cudaError_t* err) {
     return ptr;
 }
 
-// Router, capacity, experts and combine: the layer reads x, the combine adds onto res.
+// Router, capacity, experts and combine: the layer reads x, the combine adds onto res.  (The caller
+// has recorded stage event 0.)
 moe_status forward_steps(const moe_problem* p, const void* x, const void* res, const float* Wr,
                          const float* br, const ExpertWeights& W, const float* b1,
                          const float* b2, void* out, float* logits_out, int32_t* ids_out,
@@ -387,7 +393,6 @@ moe_status forward_steps(const moe_problem* p, const void* x, const void* res, c
     int32_t* rowtok = at<int32_t>(ws, q.rowtok);
     void* Y = at<void>(ws, q.Y);
 
-    stage_mark(0, s);
     // Small bf16 batches: logits on CUDA cores and routing in one launch (a 128-row tensor-core
     // tile would leave the GPU idle), then the single-block dispatch.  Larger batches: logits
     // from the tensor cores (bf16) or CUDA cores (fp32), whose launch also clears the dispatch
@@ -435,9 +440,8 @@ moe_status forward_steps(const moe_problem* p, const void* x, const void* res, c
     stage_mark(3, s);
     const long long R = max_rows_of(p, K);
     if (W.Q1) {
-        r = ffn_w4_steps(p, x, offsets, rowtok, W.Q1, b1, W.Q2, b2, Y, ws, q, s, &launches);
+        r = ffn_w4_steps(p, x, offsets, rowtok, W.Q1, b1, W.Q2, b2, Y, ws, q, s, &launches, true);
         if (r != MOE_OK) return r;
-        stage_mark(4, s);
         stage_mark(5, s);
     } else if (R > 0 && p->dtype == MOE_BF16) {
         void* H = at<void>(ws, q.H);
@@ -654,6 +658,7 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
         return MOE_ERR_INVALID_ARG;
     Plan q;
     if ((r = check_ws(p, ws, ws_bytes, &q)) != MOE_OK) return r;
+    if (p->T > 0) stage_mark(0, (cudaStream_t)stream);
     return forward_steps(p, x, x, Wr, br, ExpertWeights{W1, W2, nullptr, nullptr}, b1, b2, out,
                          logits_out, ids_out, w_out, slot_out, drop_out, counts_out, ws, q,
                          (cudaStream_t)stream, 0);
@@ -831,6 +836,7 @@ moe_status moe_forward_block(const moe_problem* p, const void* x, const moe_norm
     cudaStream_t s = (cudaStream_t)stream;
     int launches = 0;
     const void* xn = x;
+    if (p->T > 0) stage_mark(0, s);
     if (norm && p->T > 0) {
         moe::launch_layer_norm(p->dtype, x, norm->gamma, norm->beta, norm->eps, p->T, p->d_model,
                                norm->y, norm->mean, norm->rstd, s, &launches);

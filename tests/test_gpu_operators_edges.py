@@ -237,3 +237,61 @@ def test_quantize_keeps_what_is_not_finite_in_its_group(moe, dtype, zeros, group
     past = torch.arange(16 * (-(-K // 128)), device=dev())
     first = 128 * (past // 16) + 32 * (past % 4) + 8 * (past % 16 // 4)
     assert (w.q[:, :, first >= K] == -0x77777778).all()
+
+
+def stage_times(moe, call):
+    """Milliseconds of the six stages of call() (its seven events' gaps), the host well ahead."""
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(moe.STAGE_EVENTS)]
+    for e in ev:
+        e.record()                                          # (creates the handle)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(2000000)
+    moe.moe_set_stage_events(ev)
+    try:
+        call()
+    finally:
+        moe.moe_set_stage_events(None)
+    torch.cuda.synchronize()
+    return [ev[i].elapsed_time(ev[i + 1]) for i in range(6)]
+
+
+def median(values):
+    return sorted(values)[len(values) // 2]
+
+
+@pytest.mark.parametrize("T,d,F,k", [(256, 2048, 2048, 8), (4096, 1024, 1024, 4)])   # direct; read back
+def test_block_stages_of_packed_products(moe, T, d, F, k):
+    """A block over 4-bit weights records its two products, of the same weight bytes and flops, as two
+    stages (neither below a fifth of their sum)."""
+    E = 32
+    g = gen(90)
+    layer = moe.MoELayer(T, d, F, E, k, w4=True)
+    W1, W2 = make_experts(moe, g, E, F, F, d, (64, 64), False)
+    x, Wr = randn(g, T, d).to(torch.bfloat16), randn(g, d, E) / 32
+    t = [stage_times(moe, lambda: layer.forward_block(x, Wr, None, W1, None, W2, None))
+         for _ in range(7)]
+    assert 0.2 < median([v[4] / (v[3] + v[4]) for v in t]) < 0.8
+
+
+def test_block_stages_hold_the_norm(moe):
+    """The norm runs after the first event: with it the first stage is longer by the norm's time (at
+    least half of what the norm takes alone)."""
+    T, d, E = 30000, 4096, 2
+    g = gen(91)
+    layer = moe.MoELayer(T, d, 64, E, 1, 0.01)
+    x, Wr, ga = randn(g, T, d).to(torch.bfloat16), randn(g, d, E) / 64, randn(g, d)
+    W1, W2 = (randn(g, E, 64, d) / 64).to(x.dtype), (randn(g, E, d, 64) / 8).to(x.dtype)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    alone, plain, normed = [], [], []
+    for _ in range(7):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(2000000)
+        a.record()
+        layer.layer_norm(x, ga, ga)
+        b.record()
+        torch.cuda.synchronize()
+        alone.append(a.elapsed_time(b))
+        for times, norm in ((plain, None), (normed, (ga, ga, 1e-5))):
+            times.append(stage_times(moe, lambda: layer.forward_block(x, Wr, None, W1, None, W2, None,
+                                                                      norm=norm))[0])
+    assert median(normed) - median(plain) >= 0.5 * median(alone)
