@@ -92,10 +92,12 @@ Plan make_plan(const moe_problem* p) {
     q.kept_tmp = take((size_t)p->E * 4);
     q.H = take(R * p->d_ff * esize(p));
     q.Y = take(R * p->d_model * esize(p));
+    // Partial sums of the router losses and of the layer norm's parameter gradients: they lie over H
+    // and Y, which hold nothing between calls and which the calls that use them do not touch.
+    q.part = q.H;
+    off = std::max(off, align_up(q.part + std::max(moe::balance_scratch_bytes(p->T, p->E),
+                                                   moe::layer_norm_scratch_bytes(p->T, p->d_model))));
     q.split = take(p->dtype == MOE_BF16 ? moe::router_split_bytes(p->d_model, p->E) : 0);
-    // Partial sums of the router losses and of the layer norm's parameter gradients.
-    q.part = take(std::max(moe::balance_scratch_bytes(p->T, p->E),
-                           moe::layer_norm_scratch_bytes(p->T, p->d_model)));
     q.total = off;
     return q;
 }

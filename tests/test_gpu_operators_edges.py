@@ -295,3 +295,27 @@ def test_block_stages_hold_the_norm(moe):
             times.append(stage_times(moe, lambda: layer.forward_block(x, Wr, None, W1, None, W2, None,
                                                                       norm=norm))[0])
     assert median(normed) - median(plain) >= 0.5 * median(alone)
+
+
+@pytest.mark.parametrize("C", [0.01, 2.0])               # scratch larger than H and Y; smaller
+def test_training_calls_beside_a_prepared_router(moe, C):
+    """The losses' and the norm's scratch shares the workspace with a forward and with the router's
+    prepared terms: neither call's results change for the other's."""
+    T, d, F, E, k = 3000, 512, 64, 16, 2
+    g = gen(95)
+    layer = moe.MoELayer(T, d, F, E, k, C, flags=moe.FLAG_ROUTER_PREPARED)
+    plain = moe.MoELayer(T, d, F, E, k, C)
+    x, Wr, ga = randn(g, T, d).to(torch.bfloat16), randn(g, d, E) / 23, randn(g, d)
+    W1, W2 = (randn(g, E, F, d) / 23).to(x.dtype), (randn(g, E, d, F) / 8).to(x.dtype)
+    moe.moe_prepare_router(layer.p, Wr, layer.ws)
+    y, mean, rstd = layer.layer_norm(x, ga, ga)
+    logits = randn(g, T, E)
+    ids = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+    want = plain.forward(x, Wr, None, W1, None, W2, None)
+    losses, grads = plain.balance_loss(logits, ids), plain.layer_norm_backward(y, x, ga, mean, rstd)
+    for _ in range(2):
+        for a, b in zip(layer.balance_loss(logits, ids), losses):
+            assert torch.equal(a, b)
+        for a, b in zip(layer.layer_norm_backward(y, x, ga, mean, rstd), grads):
+            assert torch.equal(a, b)
+        assert torch.equal(layer.forward(x, Wr, None, W1, None, W2, None), want)

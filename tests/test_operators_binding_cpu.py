@@ -110,3 +110,16 @@ def test_arguments_of_another_kind(moe):
             call()
         assert e.value.status == moe.MOE_ERR_INVALID_ARG, n
         assert "CUDA device" not in str(e.value), n
+
+
+@pytest.mark.parametrize("args,size", [
+    ((64, 2048, 1024, 64, 8, float("inf"), "bf16", 0), 4237824),
+    ((16384, 2048, 1408, 64, 6, 1.0, "bf16", 0), 690587648),
+    ((65536, 4096, 1024, 128, 8, 1.0, "bf16", 4), 5447879936),
+    ((1, 2048, 1024, 64, 8, float("inf"), "bf16", 0), 1101568),
+    ((8, 4, 8, 4, 1, 1.25, "f32", 0), 36864),
+    ((4096, 512, 256, 1024, 2, 1.25, "f32", 0), 67269632)])
+def test_layers_pay_nothing_for_training_scratch(moe, args, size):
+    """The scratch of the losses and of the norm's parameter gradients lies over the forward's: a
+    layer's workspace is what the forward alone needs."""
+    assert moe.moe_workspace_size(moe.problem(*args)) == size
