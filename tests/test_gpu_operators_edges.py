@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from tests.gpu_util import dev
-from tests.test_gpu_operators import (U, assert_within, gen, make_experts, moe, randn,  # noqa: F401
-                                      routing, status)
+from tests.test_gpu_operators import (U, assert_within, ffn_reference, gen,  # noqa: F401
+                                      make_experts, moe, randn, routing, status, unpack)
 
 pytestmark = pytest.mark.gpu
 
@@ -319,3 +319,100 @@ def test_training_calls_beside_a_prepared_router(moe, C):
         for a, b in zip(layer.layer_norm_backward(y, x, ga, mean, rstd), grads):
             assert torch.equal(a, b)
         assert torch.equal(layer.forward(x, Wr, None, W1, None, W2, None), want)
+
+
+# ----------------------------------------------------------------------------------------------
+# Every split of the 4-bit products
+# ----------------------------------------------------------------------------------------------
+def k_split(E, max_rows, K, N):
+    """Warps that share a unit's K, as the products choose them: 2, 4 or 8."""
+    lks = 1
+    while lks < 3 and (256 << lks) <= K and min(E, max_rows) * (N // 32) < 148 * (8 >> lks):
+        lks += 1
+    return 1 << lks
+
+
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,d,F,E,k,gated,splits", [
+    (1, 2048, 128, 8, 2, False, (8, 2)), (1, 2048, 256, 8, 2, True, (8, 2)),
+    (1, 576, 640, 8, 2, False, (4, 4)), (1, 576, 640, 8, 2, True, (4, 4)),
+    (20, 1472, 1408, 4, 2, False, (8, 8)), (20, 1472, 1408, 4, 2, True, (4, 8)),
+    (20, 1472, 512, 4, 2, True, (8, 4)), (33, 960, 768, 5, 1, False, (4, 4)),
+    (7, 1024, 2048, 3, 3, True, (4, 8)), (64, 512, 1152, 8, 4, False, (4, 8)),
+    (50, 1088, 384, 30, 5, True, (2, 2))])
+def test_expert_ffn_w4_splits(moe, T, d, F, E, k, gated, splits, group, zeros):
+    """Both products, plain and gated, at every split of K, with ragged last steps, for every group
+    size and with and without offsets."""
+    g = gen(T + d + F + group)
+    F1 = 2 * F if gated else F
+    assert (k_split(E, T * k, d, F1), k_split(E, T * k, F, d)) == splits
+    W1, W2 = make_experts(moe, g, E, F1, F, d, (group, group), zeros)
+    b1, b2 = 0.1 * randn(g, E, F1), 0.1 * randn(g, E, d)
+    x = randn(g, T, d).to(torch.bfloat16)
+    offsets, rowtok = routing(g, T, E, k, "random")
+    layer = moe.MoELayer(T, d, F, E, k, flags=moe.FLAG_GATED if gated else 0, w4=True)
+    Y = layer.expert_ffn_w4(x, offsets, rowtok, W1, b1, W2, b2)
+    ref, tol = ffn_reference(x, offsets, rowtok, W1, b1, W2, b2, gated, False)
+    assert_within(Y, ref, tol, "Y")
+    assert status(moe, layer) == 0
+    assert torch.equal(Y, layer.expert_ffn_w4(x, offsets, rowtok, W1, b1, W2, b2))
+
+
+@pytest.mark.parametrize("d,F,gated,splits", [
+    (256, 128, False, (2, 2)), (256, 128, True, (2, 2)), (576, 640, False, (4, 4)),
+    (576, 640, True, (4, 4)), (1472, 1408, False, (8, 8)), (1472, 896, True, (8, 4))])
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 5, 7, 8, 9, 12, 13, 15, 16, 17, 24, 25, 31, 32, 33, 63, 64])
+def test_expert_ffn_w4_row_counts_of_each_split(moe, d, F, gated, splits, rows):
+    """Numbers of rows around the row tiles of each split (16, 8 and 4 rows), beside empty experts and
+    a full one; rows behind the last one stay as they were."""
+    T, E = 96, 5
+    g = gen(rows + d)
+    F1 = 2 * F if gated else F
+    assert (k_split(E, T, d, F1), k_split(E, T, F, d)) == splits
+    W1, W2 = make_experts(moe, g, E, F1, F, d, (64, 32), rows % 2 == 0)
+    x = randn(g, T, d).to(torch.bfloat16)
+    offsets = torch.tensor([0, 0, rows, rows, rows + 3, rows + 3], dtype=torch.int32, device=dev())
+    rowtok = torch.zeros(T, dtype=torch.int32, device=dev())
+    rowtok[:rows + 3] = torch.randint(0, T, (rows + 3,), generator=g, device=dev()).to(torch.int32)
+    layer = moe.MoELayer(T, d, F, E, 1, flags=moe.FLAG_GATED if gated else 0, w4=True)
+    Y = torch.full((T, d), 5.0, dtype=torch.bfloat16, device=dev())
+    moe.moe_expert_ffn_packed(layer.p, x, offsets, rowtok, W1.c, None, W2.c, None, Y, layer.ws)
+    ref, tol = ffn_reference(x, offsets, rowtok, W1, None, W2, None, gated, False)
+    assert_within(Y[:rows + 3], ref, tol, "Y")
+    assert (Y[rows + 3:] == 5.0).all()
+
+
+def test_block_over_packed_weights_without_rows(moe):
+    """A capacity of zero keeps no pair: the block leaves x as it is; so does a batch of no tokens."""
+    d, F, E, k = 128, 64, 4, 2
+    g = gen(97)
+    W1, W2 = make_experts(moe, g, E, F, F, d, (32, 64), True)
+    Wr, ga = randn(g, d, E), randn(g, d)
+    for T, C in ((40, 0.0), (0, 1.0)):
+        x = randn(g, T, d).to(torch.bfloat16)
+        layer = moe.MoELayer(T, d, F, E, k, C, w4=True)
+        out, r = layer.forward_block(x, Wr, None, W1, None, W2, None, norm=(ga, ga, 1e-5))
+        assert torch.equal(out, x) and (r["drop_out"] == 1).all()
+        assert status(moe, layer) == 0
+
+
+def test_read_back_of_every_scale(moe):
+    """Every bfloat16 scale (subnormal ones, infinities and NaN too) times every nibble is the float32
+    product rounded once; with an offset the float32 fused sum rounded once."""
+    bits = torch.arange(65536, device=dev(), dtype=torch.int32).to(torch.int16)
+    scale = bits.view(torch.bfloat16)
+    q = torch.zeros(1, 65536, 16, dtype=torch.int32, device=dev())
+    q[:] = torch.tensor([0x76543210, -0x01234568], dtype=torch.int32, device=dev()).repeat(8)
+    side = scale.view(1, 1, 65536).contiguous()
+    for zero in (None, side.flip(2).contiguous(), torch.full_like(side, 0.37)):
+        w = moe.W4Weights(q, side, zero, K=128, group=128)
+        # In 64 bits the product is exact, and the sum exact or, with terms more than 2^41 apart, one
+        # that rounds like the larger term alone.
+        v = unpack(q, 128).double() * scale.double().view(1, -1, 1)
+        if zero is not None:
+            v = v + zero.double().view(1, -1, 1)
+        want = v.float().to(torch.bfloat16)
+        got = moe.dequantize_w4(w)
+        same = (got == want) | (got.isnan() & want.isnan())
+        assert same.all()
