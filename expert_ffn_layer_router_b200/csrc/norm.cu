@@ -14,7 +14,10 @@
 // through a ring of cp.async stages, kRows rows ahead (a thread copies the pieces that it uses
 // itself, so no barrier guards the ring); else VB is one element (odd widths), loaded directly.
 // The variance is the two-pass one (the row is in registers, so the second pass costs no memory).
-// Statistics and sums are fp32: a lane adds at most 16 values before the tree over lanes and warps.
+// Statistics and sums are fp32.  Of a row's statistics a lane adds at most 16 values before the tree
+// over lanes and warps (d / 512 in the *_wide kernels); of dgamma and dbeta a thread adds its rows
+// behind one another, rows / (296 row groups of a block) (rows / 16 in the wide kernel), before the
+// partial rows are joined: 222 at 65536 x 4096.
 // (65536 x 4096 bfloat16.  Forward 174 us, 164 at the copy bandwidth; with gamma and beta read for
 // every row, which kept the load unit at 76%, 234.  Backward with the residual 346 us, 327 at the copy
 // bandwidth; with rows loaded when they were needed, and the residual's after the sums, 566.)

@@ -465,8 +465,13 @@ def dequantize_w4(w: W4Weights, stream=None):
 class MoELayer:
     """Holds a problem description and a workspace; calls the C ABI on torch tensors.
 
+    The workspace serves one call at a time: calls of one layer that may overlap on the GPU (on
+    other streams) take a layer each.
+
     ``w4``: size the workspace for 4-bit expert weights too (``expert_ffn_w4``,
-    ``forward_block`` with :class:`W4Weights`)."""
+    ``forward_block`` with :class:`W4Weights`); above 64 rows an expert that adds a bfloat16 copy of
+    the larger weight.  (Weights are arguments: one object serves all layers of a model that have
+    this shape and run one after the other, and so one workspace does.)"""
 
     def __init__(self, T, d_model, d_ff, E, k, capacity_factor=math.inf, dtype="bf16",
                  device="cuda", flags=0, w4=False):

@@ -23,7 +23,9 @@
  *   - All pointers except `p` and the out-parameters of the host-only queries are DEVICE
  *     pointers owned by the caller.  The library never allocates device memory: scratch comes
  *     from the caller's workspace `ws` of `ws_bytes` bytes (size from moe_workspace_size,
- *     256-byte aligned).
+ *     256-byte aligned).  A workspace serves one call at a time: calls that share one are ordered
+ *     (on one stream, or by events); calls that may overlap, on other streams or in graphs replayed
+ *     at once, take a workspace each.
  *   - Every compute call is asynchronous on `stream` (a cudaStream_t; NULL = legacy default
  *     stream) and performs no host synchronisation.  Kernels are launched with programmatic
  *     stream serialization: a kernel may be scheduled while the preceding work on `stream`
@@ -264,7 +266,8 @@ moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes);
  * moe_expert_ffn's rules for widths, alignment, offsets and rowtok; rows of Y behind offsets[E] are
  * left as they were.
  * Few rows per expert (min(T k, E K) <= 64 E): the products read the 4-bit weights and form
- * sum_k (nibble - 8) x_k per group exactly in float32 before the scale; b1, b2 nullable.  More rows:
+ * sum_k (nibble - 8) x_k per group, of exact products added in float32, before the scale; b1, b2
+ * nullable.  More rows:
  * each weight is first read back to bfloat16 (one rounding per value) into the workspace, for the
  * grouped tensor-core GEMM.  The hidden activations are kept in bfloat16 either way. */
 moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int32_t* offsets,
@@ -275,9 +278,10 @@ moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int3
 /* ---- Layer norm ----------------------------------------------------------------------------
  * y = gamma (x - mean) rstd + beta per token, rstd = 1 / sqrt(variance + eps), the variance over
  * d_model without bias correction.  x, y [T, d_model] in p's dtype, any d_model; gamma, beta
- * [d_model] float32; mean, rstd [T] float32 out.  eps >= 0 and finite (with eps = 0 a row of equal
- * values gives NaN; where a float32 variance overflows, rstd is 0 and y is beta); d_model at most 2^30.  y must not alias x.  Statistics are float32, y is
- * rounded once. */
+ * [d_model] float32; mean, rstd [T] float32 out.  eps >= 0 and finite (with eps = 0 the y of a row of
+ * equal values is undefined: the rounding of its mean decides; where a float32 variance overflows but
+ * the row's sum does not, rstd is 0 and y is beta); d_model at most 2^30.  y must not alias x.
+ * Statistics are float32, y is rounded once. */
 moe_status moe_layer_norm(const moe_problem* p, const void* x, const float* gamma,
                           const float* beta, float eps, void* y, float* mean, float* rstd,
                           void* stream);

@@ -416,3 +416,61 @@ def test_read_back_of_every_scale(moe):
         got = moe.dequantize_w4(w)
         same = (got == want) | (got.isnan() & want.isnan())
         assert same.all()
+
+
+# ----------------------------------------------------------------------------------------------
+# Long sums, against bounds of the depth they have
+# ----------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("T,E,k,groups", [(1 << 21, 8, 2, 64), (1 << 20, 64, 6, 64), (1 << 18, 1024, 4, 8)])
+def test_balance_loss_of_many_tokens(moe, T, E, k, groups):
+    """Large batches: 256 blocks of `groups` tokens at a time, so a lane adds T / (256 groups)
+    probabilities behind one another; the lanes, warps (16), cluster (8) and clusters (32) follow, at
+    most 64 more."""
+    g = gen(E)
+    logits = 2 * randn(g, T, E)
+    ids = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+    layer = moe.MoELayer(T, 64, 64, E, k, 0.001)
+    losses, counts, probs = layer.balance_loss(logits, ids)
+    P, z, span = torch.zeros(E, dtype=torch.float64, device=dev()), 0.0, 0.0
+    for L in logits.split(1 << 16):
+        L = L.double()
+        lse = torch.logsumexp(L, 1)
+        P += torch.exp(L - lse[:, None]).sum(0)
+        z += (lse ** 2).sum()
+        span = max(span, (L.amax(1) - L.amin(1)).max().item())
+    n = torch.bincount(ids.reshape(-1).long(), minlength=E)
+    P, z = P / T, z / T
+    assert torch.equal(counts.long(), torch.cat([n, torch.tensor([T], device=dev())]))
+    # A probability's own error as in the operators' main tests, and the sum over the tokens.
+    b = 2 * (span + 45) + T // (256 * groups) + 64
+    assert_within(probs, P, b * U * P, "probs")
+    bal = E * (n.double() / (T * k) * P).sum()
+    # (sum over the experts: a thread's one or two, 5 tree steps, the warps; lse's error is that of the
+    # exponentials' sum plus its own two roundings, twice in its square)
+    assert_within(losses[:1], bal[None], (b + 64) * U * bal, "balance loss")
+    assert_within(losses[1:], z[None], (2 * (span + 45) / z ** 0.5 + b + 8) * 2 * U * z, "z-loss")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d,depth", [(200000, 512, 200000 // (296 * 8) + 64),
+                                       (50000, 4096, 50000 // 296 + 64),
+                                       (20000, 8200, 20000 // 16 + 64)])
+def test_layer_norm_parameter_sums_of_many_rows(moe, dtype, T, d, depth):
+    """dgamma and dbeta: a thread adds its rows behind one another (of 296 blocks and the rows a block
+    has in flight; a sixteenth of all rows past 8192 columns), then the blocks' partial rows."""
+    g = gen(d)
+    x, dy = randn(g, T, d).to(dtype), randn(g, T, d).to(dtype)
+    gamma = randn(g, d)
+    mean, rstd = x.float().mean(1), 1 / x.float().std(1)
+    layer = moe.MoELayer(T, d, 64, 1, 1, dtype="f32" if dtype == torch.float32 else "bf16")
+    _, dgamma, dbeta = layer.layer_norm_backward(dy, x, gamma, mean, rstd)
+    ref = [torch.zeros(d, dtype=torch.float64, device=dev()) for _ in range(4)]
+    for r in range(0, T, 8192):
+        s = slice(r, r + 8192)
+        xh = (x[s].double() - mean[s, None].double()) * rstd[s, None].double()
+        y = dy[s].double()
+        for acc, v in zip(ref, (y * xh, (y * xh).abs(), y, y.abs())):
+            acc += v.sum(0)
+    # (x - mean) rstd: two roundings.
+    assert_within(dgamma, ref[0], (depth + 3) * U * ref[1], "dgamma")
+    assert_within(dbeta, ref[2], depth * U * ref[3], "dbeta")
