@@ -225,7 +225,9 @@ int w4_rows1(const moe_problem* p) {          // rows of W1 per expert
 // Rows per expert (the batch's largest average) up to which the products read the 4-bit weights
 // directly; above it the weights are first read back to bfloat16 for the tensor-core GEMM.  (64
 // experts of 2048 x 1024, both products, direct and read back: 16 rows 84 and 216 us, 48 rows 173 and
-// 219, 64 rows 228 and 238, 96 rows 327 and 226.)
+// 219, 64 rows 228 and 238, 96 rows 327 and 226.  With offsets and groups of 128 at 2048 x 1408: 48
+// rows 269 and 72 rows 312, read back.  Gated, with offsets and groups of 32, the two meet earlier: 48
+// rows 473, 72 rows 462, read back.  bfloat16 weights are faster than either from 18 to 24 rows on.)
 constexpr long long kW4DirectRows = 64;
 
 bool w4_direct(const moe_problem* p) {

@@ -308,15 +308,20 @@ __global__ void __launch_bounds__(256)
 // more.
 //
 // Measured, 64 experts of 2048 x 1024 (134 million weights, 72 MB with scales of 64 columns), 64
-// tokens, 8 experts each: 28-31 us a product, 2.5 TB/s of weights.  What bounds it is the instructions
-// of a chunk (4096 weights): about 400, of which the unpacking takes 176 (7 of the integer unit, which
-// starts one every second cycle, and 4 of the half-precision one a word), issued at 45-50% with the 5
-// warps per scheduler that 96 registers leave room for.  The copies alone take 16 us.  On the way:
+// tokens, 8 experts each: 28-31 us a product, 2.5 TB/s of weights.  What bounds it is the
+// chain of a chunk (4096 weights: barrier, loads from shared memory, unpacking, products) with the 5
+// warps per scheduler that 96 registers leave room for: its instructions, about 400, of which the
+// unpacking takes 176 (7 of the integer unit, which starts one every second cycle, and 4 of the
+// half-precision one a word), are issued in 45-50% of the cycles.  The copies alone take 16 us.  More
+// than 16 rows of an expert are more units, each of which unpacks its weights again: the time grows
+// with the rows (both products: 82 us at 16 rows, 136 at 32, 225 at 64).  On the way:
 // K split over all 8 warps with rows from global memory 78 us; group sizes as template arguments (a
 // runtime division is 30 instructions) 37; rows through the L1 cache 41; 16 product warps in one block
 // per SM 33; KS as a template argument too: 4-6% less at every batch; a unit's offsets from shared
 // memory: 1-3% less.  Unpacking into tensor memory for tcgen05 products was tried and took 42: at 16
 // rows a product of 16 columns takes 40 cycles, and the barriers of a 16 KB stage half a microsecond.
+// (At 32 rows an expert, where this kernel unpacks a weight twice, it was the faster one: 120 against
+// 139 us for both products.)
 // ------------------------------------------------------------------------------------------------
 enum W4Epi { kW4SiLU = 0, kW4Bias = 1, kW4SwiGLU = 2 };
 
