@@ -385,7 +385,6 @@ class W4Weights:
     moe_w4).  :func:`quantize_w4` makes them.  The tensors' values may change in place; other
     tensors take another object."""
 
-    __slots__ = ("_tensors", "_shapes", "_sizes", "_device")
     q = property(lambda self: self._tensors[0])
     scale = property(lambda self: self._tensors[1])
     zero = property(lambda self: self._tensors[2])
