@@ -245,7 +245,8 @@ moe_status moe_forward(const moe_problem* p, const void* x, const float* Wr, con
  * not finite and reads back as values that are not finite; the other groups do not see it.
  * Per group, zero = NULL: scale = max|w| / 7; else scale = (max - min) / 15 and zero = min + 8 scale.
  * Both are rounded to bfloat16 first (the differences, products with the float32 reciprocal of 7 or
- * 15, and sums in float32), then nibble - 8 = round-half-even((w - zero) / scale), clamped to [-8, 7]; 0 where scale = 0.
+ * 15, and sums in float32), then nibble - 8 = round-half-even((w - zero) / scale), clamped to
+ * [-8, 7]; 0 where scale = 0.
  * K must be a multiple of 64 and at most 2^30, N at most 2097120 and E at most 65535 (else
  * MOE_ERR_UNSUPPORTED). */
 moe_status moe_quantize_packed(const void* W, int32_t dtype, int32_t E, int32_t N, int32_t K,
@@ -268,7 +269,8 @@ moe_status moe_workspace_size_packed(const moe_problem* p, size_t* bytes);
  * Few rows per expert (min(T k, E K) <= 64 E): the products read the 4-bit weights and form
  * sum_k (nibble - 8) x_k per group, of exact products added in float32, before the scale; b1, b2
  * nullable.  More rows: each weight is first read back to bfloat16 (one rounding per value) into the
- * workspace, for the grouped tensor-core GEMM.  The hidden activations are kept in bfloat16 either way. */
+ * workspace, for the grouped tensor-core GEMM.  The hidden activations are kept in bfloat16 either
+ * way. */
 moe_status moe_expert_ffn_packed(const moe_problem* p, const void* x, const int32_t* offsets,
                              const int32_t* rowtok, const moe_w4* W1, const float* b1,
                              const moe_w4* W2, const float* b2, void* Y, void* ws,
@@ -316,7 +318,8 @@ moe_status moe_balance_loss(const moe_problem* p, const float* logits, const int
  * constant).  MOE_FLAG_RENORMALIZE: the weights are the renormalised ones, a softmax over the k
  * named logits wherever these lie in the row (named experts of -infinity have weight 0; where all
  * are, this part is 0).  At least one of the two is given.  An id outside [0, E) is left out and
- * recorded as MOE_DEV_BAD_INDEX; an id named twice by a token adds up.  dlogits must not alias logits. */
+ * recorded as MOE_DEV_BAD_INDEX; an id named twice by a token adds up.  dlogits must not alias
+ * logits. */
 moe_status moe_route_backward(const moe_problem* p, const float* logits, const int32_t* ids,
                               const uint8_t* mask, const int32_t* counts,
                               const float* grad_losses, const float* grad_w, float* dlogits,
